@@ -284,6 +284,94 @@ lowram_status lowram_append(lowram_ctx* dst_ctx, const lowram_cache* dst,
                             const lowram_ctx* block_ctx, const lowram_cache* block,
                             void* stream);
 
+/* ---- A paged cache in 8 bits ------------------------------------------------------
+ * Generated tokens (or a whole uncompressed context) held in pages of page_tokens tokens,
+ * one byte an element, with one scale for each (page, KV head) of the keys and one of the
+ * values. It serves ragged batches: every sequence has its own length and page list.
+ *   k_code, v_code   [n_pages][H_kv][page_tokens][d] e4m3 codes (4 exponent bits, 3 fraction
+ *                    bits, no infinities, 0x7f / 0xff = NaN);
+ *   k_scale, v_scale [n_pages][H_kv] fp32, positive: value = code * scale. lowram_paged_append
+ *                    writes powers of two 2^e, -64 <= e <= 120; scales written elsewhere must
+ *                    lie in that range;
+ *   table            [n_seqs][max_pages] int32: token t of sequence b is row t % page_tokens of
+ *                    page table[b][t / page_tokens]. Entries past a sequence's last page are
+ *                    never read;
+ *   lens             [n_seqs] int32 tokens of each sequence, 0 .. max_pages * page_tokens. In
+ *                    lowram_paged_append they count the tokens that the call appends.
+ * page_tokens is 16, 32 or 64; n_pages * H_kv * page_tokens < 2^31 and max_pages * page_tokens
+ * <= 2^24 (LOWRAM_ERR_UNSUPPORTED otherwise); n_seqs 1 .. 8192, independent of the context's
+ * batch. Of the context the calls use n_kv_heads, n_q_heads, head_dim, dtype (fp32 or bf16),
+ * rope_theta and the device. Sequences may share pages that are only read; a page that an
+ * append writes belongs to one sequence (not checked: the rows of the other sequence are then
+ * overwritten).
+ * Lengths and page indices are read on the device. A length outside 0 .. max_pages *
+ * page_tokens is cut to that range, and tokens of a page index outside 0 .. n_pages-1 are
+ * skipped (attend: masked; gather: zeros; append: dropped); both are reported by
+ * lowram_last_error as LOWRAM_ERR_DEVICE_CHECK. */
+typedef struct lowram_pages {
+  void* k_code;
+  void* v_code;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_tokens;
+} lowram_pages;
+
+/* Append new keys and values to the pages, rotating the keys by their positions on the way
+ * (long generation keeps the generated suffix beside the compressed prefix: agihunt summary,
+ * limitations paragraph).
+ *   k_new, v_new [n_new][H_kv][d] in cfg->dtype; consecutive tokens k_stride / v_stride
+ *           elements apart (>= H_kv * d, a multiple of 16 bytes), so slices of a fused
+ *           projection's output can be passed as they are;
+ *   cu_new  [n_seqs + 1] int32 (device): the rows cu_new[b] .. cu_new[b+1]-1 are sequence b's
+ *           new tokens, max_new (host) at least the largest count. NULL: n_new / n_seqs rows
+ *           for every sequence (n_new % n_seqs == 0; max_new is ignored);
+ *   pos_base [n_seqs] int32 (device) or NULL (0): token t of sequence b has position
+ *           pos_base[b] + t, 0 .. 2^24 - 1 (behind a compressed prefix: its length);
+ *   rotate  1: k_new is pre-RoPE and is rotated (rotate-half, angles and products in fp64,
+ *           rounded to fp32); 0: k_new is stored as given.
+ * Sequence b's n_b new tokens become tokens lens[b] - n_b .. lens[b] - 1. For every (page,
+ * head) touched, keys and values apart: with amax the largest finite magnitude written,
+ * the scale is the smallest 2^e, e >= -64, with amax <= 448 * 2^e, or the scale the page has
+ * if that is larger and the page holds earlier tokens of the sequence; their codes are then
+ * rounded again to the larger scale (exact unless the result is subnormal, below 2^-6). Codes
+ * are e4m3(x / scale), to nearest even; infinities and NaN become NaN codes. Rows behind the
+ * last new token keep their bytes. Calling again with the same inputs changes nothing.
+ * A sequence whose counts are malformed (cu_new out of order or range, more than max_new
+ * tokens, lens[b] < n_b or above max_pages * page_tokens, a position out of range) is left
+ * alone and reported as LOWRAM_ERR_DEVICE_CHECK. n_new == 0 is allowed. No workspace. */
+lowram_status lowram_paged_append(lowram_ctx* ctx, const lowram_pages* pages, const void* k_new,
+                                  const void* v_new, int64_t k_stride, int64_t v_stride,
+                                  int32_t n_new, const int32_t* cu_new, int32_t max_new,
+                                  const int32_t* pos_base, int32_t rotate, void* stream);
+
+/* Exact GQA attention over the paged cache for the last n_q (1 .. 16) tokens of every
+ * sequence, with scale 1/sqrt(d):
+ *   q, out [n_seqs][n_q][H_q][d] (post-RoPE queries; out written); lse [n_seqs][n_q][H_q]
+ *   fp32 (written when not NULL): the natural logarithm of the softmax's sum.
+ * Query j of sequence b is its token lens[b] - n_q + j and sees tokens 0 .. lens[b] - n_q + j.
+ * A query that sees none (an empty sequence) gets out = 0 and lse = -inf.
+ * Bytes of rows behind a sequence's length may be anything (NaN codes too). Workspace:
+ * lowram_paged_workspace_size(cfg, n_seqs, n_q). */
+lowram_status lowram_paged_attend(lowram_ctx* ctx, const lowram_pages* pages, const void* q,
+                                  int32_t n_q, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+lowram_status lowram_paged_workspace_size(const lowram_config* cfg, int32_t n_seqs, int32_t n_q,
+                                          size_t* bytes);
+
+/* Read a run of tokens back out of the pages: k_out, v_out [n_seqs][n][H_kv][d] in cfg->dtype,
+ * row i of sequence b is token start[b] + i (start NULL: 0) as code * scale, rounded to the
+ * dtype (a scaled e4m3 code is exact in bf16 unless it is below bf16's normal range); rows
+ * outside 0 .. lens[b] - 1 are zeros. This is the layout lowram_encode takes: a block of the
+ * generated suffix goes from the pages to a compressed block for lowram_append. */
+lowram_status lowram_paged_gather(lowram_ctx* ctx, const lowram_pages* pages,
+                                  const int32_t* start, int32_t n, void* k_out, void* v_out,
+                                  void* stream);
+
 /* Decode sub-step 1 (kernel (a) alone): score every chunk by max over the GQA group of
  * q . landmark and write the top-k chunks per (batch, KV head), ascending, ties to the
  * lower chunk (agihunt summary, key paragraph; cctest "Selective reconstruction").

@@ -29,6 +29,8 @@ struct lowram_ctx {
   int* item_ctr;  // device [H]: tile counters of the tcgen05 attend kernel, 0 between calls
   double* theta64;  // device [d/2]
   float2* chunk32;  // device [T/C][d/2]: (cos, sin)(c C theta_i)
+  double2* mid64;   // device [2^8][d/2], [2^7][d/2]: third RoPE level (RopeTables)
+  double2* top64;
 };
 
 namespace {
@@ -145,6 +147,8 @@ RopeTables rope_of(const lowram_ctx* ctx) {
   r.half = ctx->cfg.head_dim / 2;
   r.theta64 = ctx->theta64;
   r.chunk32 = ctx->chunk32;
+  r.mid64 = ctx->mid64;
+  r.top64 = ctx->top64;
   return r;
 }
 
@@ -287,6 +291,8 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
   std::vector<double> th64((size_t)half);
   const size_t n_chunks = (size_t)(n_pos / c->chunk);
   std::vector<float2> chunk32(n_chunks * half);
+  constexpr int kMid = 1 << kRopeMidBits, kTop = 1 << kRopeTopBits;
+  std::vector<double2> mid64((size_t)half * kMid), top64((size_t)half * kTop);
   for (int i = 0; i < half; ++i) {
     const double th = std::pow(c->rope_theta, -2.0 * i / c->head_dim);
     th64[i] = th;
@@ -304,6 +310,14 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
       const double ang = (double)(cc * (size_t)c->chunk) * th;
       chunk32[cc * half + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
     }
+    for (int j = 0; j < kMid; ++j) {
+      const double ang = (double)(j << kRopeLoBits) * th;
+      mid64[(size_t)j * half + i] = make_double2(std::cos(ang), std::sin(ang));
+    }
+    for (int j = 0; j < kTop; ++j) {
+      const double ang = (double)(j << (kRopeLoBits + kRopeMidBits)) * th;
+      top64[(size_t)j * half + i] = make_double2(std::cos(ang), std::sin(ang));
+    }
   }
   const size_t pairs = (size_t)c->batch * c->n_kv_heads;
   bool ok = cudaMalloc(&ctx->lo32, lo32.size() * sizeof(float2)) == cudaSuccess &&
@@ -316,7 +330,9 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
             cudaMalloc(&ctx->item_ctr, (size_t)c->n_kv_heads * sizeof(int)) == cudaSuccess &&
             cudaMalloc(&ctx->scores, pairs * (size_t)(c->n_tokens / c->chunk) * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->theta64, th64.size() * sizeof(double)) == cudaSuccess &&
-            cudaMalloc(&ctx->chunk32, chunk32.size() * sizeof(float2)) == cudaSuccess;
+            cudaMalloc(&ctx->chunk32, chunk32.size() * sizeof(float2)) == cudaSuccess &&
+            cudaMalloc(&ctx->mid64, mid64.size() * sizeof(double2)) == cudaSuccess &&
+            cudaMalloc(&ctx->top64, top64.size() * sizeof(double2)) == cudaSuccess;
   ok = ok &&
        cudaMemcpy(ctx->lo32, lo32.data(), lo32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
        cudaMemcpy(ctx->hi32, hi32.data(), hi32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
@@ -328,7 +344,9 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
        cudaMemset(ctx->item_ctr, 0, (size_t)c->n_kv_heads * sizeof(int)) == cudaSuccess &&
        cudaMemset(ctx->scores, 0xff, pairs * (size_t)(c->n_tokens / c->chunk) * sizeof(float)) == cudaSuccess &&
        cudaMemcpy(ctx->theta64, th64.data(), th64.size() * sizeof(double), cudaMemcpyHostToDevice) == cudaSuccess &&
-       cudaMemcpy(ctx->chunk32, chunk32.data(), chunk32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess;
+       cudaMemcpy(ctx->chunk32, chunk32.data(), chunk32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
+       cudaMemcpy(ctx->mid64, mid64.data(), mid64.size() * sizeof(double2), cudaMemcpyHostToDevice) == cudaSuccess &&
+       cudaMemcpy(ctx->top64, top64.data(), top64.size() * sizeof(double2), cudaMemcpyHostToDevice) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
     lowram_destroy(ctx);
@@ -352,6 +370,8 @@ void lowram_destroy(lowram_ctx* ctx) {
   cudaFree(ctx->item_ctr);
   cudaFree(ctx->theta64);
   cudaFree(ctx->chunk32);
+  cudaFree(ctx->mid64);
+  cudaFree(ctx->top64);
   delete ctx;
 }
 
@@ -788,6 +808,146 @@ lowram_status lowram_decode_step_suffix(lowram_ctx* ctx, const lowram_cache* cac
     return st;
   if (launch_suffix_merge(dm, k_suffix, v_suffix, s_max, n_suffix, q, pre_out, pre_ml, out,
                           ws + sw.part, ctx->status, s) != cudaSuccess) {
+    cudaGetLastError();
+    return LOWRAM_ERR_CUDA;
+  }
+  return LOWRAM_OK;
+}
+
+}  // extern "C"
+
+namespace {
+
+// Host checks of a paged cache against a context's configuration.
+lowram_status check_pages(const lowram_pages* p, const lowram_config& c) {
+  if (!p || !p->k_code || !p->v_code || !p->k_scale || !p->v_scale || !p->table || !p->lens)
+    return LOWRAM_ERR_INVALID_ARG;
+  if (p->n_seqs < 1 || p->max_pages < 1 || p->n_pages < 1 || p->page_tokens < 1)
+    return LOWRAM_ERR_SHAPE;
+  if (!pow2_in(p->page_tokens, 16, 64) || p->n_seqs > kPagedMaxSeqs) return LOWRAM_ERR_UNSUPPORTED;
+  // rows are TMA coordinates (int32); lengths are RoPE positions
+  if ((int64_t)p->n_pages * c.n_kv_heads * p->page_tokens >= ((int64_t)1 << 31))
+    return LOWRAM_ERR_UNSUPPORTED;
+  if ((int64_t)p->max_pages * p->page_tokens > kMaxPosition) return LOWRAM_ERR_UNSUPPORTED;
+  if (!aligned16(p->k_code) || !aligned16(p->v_code) || !aligned16(p->k_scale) ||
+      !aligned16(p->v_scale) || !aligned16(p->table) || !aligned16(p->lens))
+    return LOWRAM_ERR_ALIGN;
+  return LOWRAM_OK;
+}
+
+PagedArgs paged_args(const lowram_ctx* ctx, const lowram_pages* p) {
+  const lowram_config& c = ctx->cfg;
+  PagedArgs a{};
+  a.H = c.n_kv_heads;
+  a.Hq = c.n_q_heads;
+  a.G = c.n_q_heads / c.n_kv_heads;
+  a.d = c.head_dim;
+  a.dtype = c.dtype;
+  a.pg = *p;
+  a.rope = rope_of(ctx);
+  a.status = ctx->status;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+lowram_status lowram_paged_append(lowram_ctx* ctx, const lowram_pages* pages, const void* k_new,
+                                  const void* v_new, int64_t k_stride, int64_t v_stride,
+                                  int32_t n_new, const int32_t* cu_new, int32_t max_new,
+                                  const int32_t* pos_base, int32_t rotate, void* stream) {
+  if (!ctx || (rotate != 0 && rotate != 1)) return LOWRAM_ERR_INVALID_ARG;
+  const lowram_config& c = ctx->cfg;
+  lowram_status st = check_pages(pages, c);
+  if (st != LOWRAM_OK) return st;
+  if (n_new < 0) return LOWRAM_ERR_SHAPE;
+  if (n_new == 0) return LOWRAM_OK;
+  if (!k_new || !v_new) return LOWRAM_ERR_INVALID_ARG;
+  if (!cu_new && n_new % pages->n_seqs != 0) return LOWRAM_ERR_SHAPE;
+  if (cu_new && (max_new < 1 || max_new > n_new)) return LOWRAM_ERR_SHAPE;
+  const int64_t row = (int64_t)c.n_kv_heads * c.head_dim;
+  if (k_stride < row || v_stride < row) return LOWRAM_ERR_SHAPE;
+  const int64_t es = (int64_t)elem_size(c);
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(cu_new) || !aligned16(pos_base) ||
+      k_stride * es % 16 != 0 || v_stride * es % 16 != 0)
+    return LOWRAM_ERR_ALIGN;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return LOWRAM_ERR_CUDA;
+  PagedArgs a = paged_args(ctx, pages);
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.n_new = n_new;
+  a.cu_new = cu_new;
+  a.max_new = cu_new ? max_new : n_new / pages->n_seqs;
+  a.pos_base = pos_base;
+  a.rotate = rotate;
+  if (launch_paged_append(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return LOWRAM_ERR_CUDA;
+  }
+  return LOWRAM_OK;
+}
+
+lowram_status lowram_paged_workspace_size(const lowram_config* c, int32_t n_seqs, int32_t n_q,
+                                          size_t* bytes) {
+  if (!bytes) return LOWRAM_ERR_INVALID_ARG;
+  const lowram_status st = lowram_check_config(c);
+  if (st != LOWRAM_OK) return st;
+  if (n_seqs < 1 || n_q < 1) return LOWRAM_ERR_SHAPE;
+  if (n_seqs > kPagedMaxSeqs || n_q > kPagedMaxQueries) return LOWRAM_ERR_UNSUPPORTED;
+  *bytes = paged_attend_workspace_bytes(c->n_kv_heads, c->n_q_heads / c->n_kv_heads, c->head_dim,
+                                        c->dtype, n_seqs, n_q);
+  return LOWRAM_OK;
+}
+
+lowram_status lowram_paged_attend(lowram_ctx* ctx, const lowram_pages* pages, const void* q,
+                                  int32_t n_q, void* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  if (!ctx || !q || !out || !workspace) return LOWRAM_ERR_INVALID_ARG;
+  const lowram_config& c = ctx->cfg;
+  lowram_status st = check_pages(pages, c);
+  if (st != LOWRAM_OK) return st;
+  size_t need = 0;
+  if ((st = lowram_paged_workspace_size(&c, pages->n_seqs, n_q, &need)) != LOWRAM_OK) return st;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(lse) || !aligned16(workspace))
+    return LOWRAM_ERR_ALIGN;
+  if (workspace_bytes < need) return LOWRAM_ERR_WORKSPACE;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return LOWRAM_ERR_CUDA;
+  PagedArgs a = paged_args(ctx, pages);
+  a.q = q;
+  a.out = out;
+  a.lse = lse;
+  a.n_q = n_q;
+  a.ws = static_cast<float*>(workspace);
+  if (launch_paged_attend(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return LOWRAM_ERR_CUDA;
+  }
+  return LOWRAM_OK;
+}
+
+lowram_status lowram_paged_gather(lowram_ctx* ctx, const lowram_pages* pages,
+                                  const int32_t* start, int32_t n, void* k_out, void* v_out,
+                                  void* stream) {
+  if (!ctx) return LOWRAM_ERR_INVALID_ARG;
+  const lowram_status st = check_pages(pages, ctx->cfg);
+  if (st != LOWRAM_OK) return st;
+  if (n < 0 || n > kMaxPosition) return LOWRAM_ERR_SHAPE;
+  if (n == 0) return LOWRAM_OK;
+  if (!k_out || !v_out) return LOWRAM_ERR_INVALID_ARG;
+  if (!aligned16(start) || !aligned16(k_out) || !aligned16(v_out)) return LOWRAM_ERR_ALIGN;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return LOWRAM_ERR_CUDA;
+  PagedArgs a = paged_args(ctx, pages);
+  a.start = start;
+  a.n = n;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  if (launch_paged_gather(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return LOWRAM_ERR_CUDA;
   }

@@ -35,7 +35,14 @@ struct RopeTables {
   // chunk-base rotations: chunk32[c * half + i] = (cos, sin)(c C theta_i), c < T / C,
   // from fp64 on the host
   const float2* chunk32;
+  // third level, for positions behind the prefix (any position < 2^24 = top, mid, lo bits):
+  //   mid64[j * half + i] = (cos, sin)(j 2^9 theta_i), j < 2^8
+  //   top64[j * half + i] = (cos, sin)(j 2^17 theta_i), j < 2^7
+  const double2* mid64;
+  const double2* top64;
 };
+constexpr int kRopeMidBits = 8, kRopeTopBits = 7;
+constexpr int kMaxPosition = 1 << (kRopeLoBits + kRopeMidBits + kRopeTopBits);
 
 struct Dims {
   int B, T, H, Hq, G, d, r, C, F, Nc, k, n_res, act, dtype;
@@ -204,6 +211,31 @@ struct AppendArgs {
   int* status;
 };
 cudaError_t launch_append(const AppendArgs& a, int num_sms, cudaStream_t s);
+
+// ---------------- paged 8-bit cache ----------------
+constexpr int kPagedMaxSeqs = 8192;
+constexpr int kPagedMaxQueries = 16;
+struct PagedArgs {
+  int H, Hq, G, d, dtype;
+  lowram_pages pg;
+  RopeTables rope;
+  int* status;
+  // append
+  const void* k_new; const void* v_new;
+  int64_t k_stride, v_stride;     // elements between consecutive tokens
+  int n_new, max_new, rotate;
+  const int32_t* cu_new;          // or null: n_new / n_seqs tokens each
+  const int32_t* pos_base;        // or null
+  // attend
+  const void* q; void* out; float* lse; int n_q;
+  float* ws;
+  // gather
+  const int32_t* start; int n; void* k_out; void* v_out;
+};
+cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_paged_gather(const PagedArgs& a, int num_sms, cudaStream_t s);
+size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q);
+cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s);
 
 // 2D tiled TMA map over a row-major [rows][cols] array of dtype (LOWRAM_DTYPE_*), box
 // box_rows x box_cols, swizzle 0/32/64/128 bytes; L2 fetches promoted to l2_promo bytes

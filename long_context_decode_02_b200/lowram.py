@@ -71,6 +71,14 @@ class lowram_cache(ctypes.Structure):
                 ("chunk_pos", ctypes.c_void_p), ("res_scale", ctypes.c_void_p)]
 
 
+class lowram_pages(ctypes.Structure):
+    _fields_ = [("k_code", ctypes.c_void_p), ("v_code", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
 _S = ctypes.c_int
 _sig = {
@@ -109,6 +117,15 @@ _sig = {
                               ctypes.c_int32, ctypes.c_int32, _P, _P, ctypes.c_size_t, _P]),
     "lowram_fit_basis_workspace_size": (_S, [ctypes.POINTER(lowram_config), ctypes.c_int32,
                                              ctypes.POINTER(ctypes.c_size_t)]),
+    "lowram_paged_append": (_S, [_P, ctypes.POINTER(lowram_pages), _P, _P, ctypes.c_int64,
+                                 ctypes.c_int64, ctypes.c_int32, _P, ctypes.c_int32, _P,
+                                 ctypes.c_int32, _P]),
+    "lowram_paged_attend": (_S, [_P, ctypes.POINTER(lowram_pages), _P, ctypes.c_int32, _P, _P,
+                                 _P, ctypes.c_size_t, _P]),
+    "lowram_paged_workspace_size": (_S, [ctypes.POINTER(lowram_config), ctypes.c_int32,
+                                         ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "lowram_paged_gather": (_S, [_P, ctypes.POINTER(lowram_pages), _P, ctypes.c_int32, _P, _P,
+                                 _P]),
     "lowram_debug_reconstruct": (_S, [_P, ctypes.POINTER(lowram_cache),
                                       ctypes.POINTER(lowram_layer_params), _P, _P, _P, _P, _P,
                                       _P, _P, ctypes.c_size_t, _P]),
@@ -187,6 +204,7 @@ class Context:
 
     def __init__(self, cfg: lowram_config, device: int = 0):
         self.cfg = cfg
+        self.device = device
         self._h = ctypes.c_void_p()
         check(lowram_create(ctypes.byref(cfg), device, ctypes.byref(self._h)), "lowram_create")
 
@@ -386,3 +404,162 @@ def decode_step_suffix(ctx: Context, cache: dict, params: lowram_layer_params, q
                                     _ptr(out), _ptr(sel_out), _ptr(workspace),
                                     workspace.numel() * workspace.element_size(), _stream(stream)),
           "lowram_decode_step_suffix")
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+def alloc_pages(cfg: lowram_config, n_pages: int, page_tokens: int, device) -> dict:
+    """Device tensors of a paged 8-bit cache (shapes of include/lowram.h). The codes are e4m3
+    bytes: ``codes.view(torch.float8_e4m3fn)`` gives their values."""
+    import torch
+    H, d = cfg.n_kv_heads, cfg.head_dim
+    out = {}
+    for n in ("k", "v"):
+        out[n + "_code"] = torch.empty(n_pages, H, page_tokens, d, dtype=torch.uint8,
+                                       device=device)
+        out[n + "_scale"] = torch.empty(n_pages, H, dtype=torch.float32, device=device)
+    return out
+
+
+def paged_cache(k_code, v_code, k_scale, v_scale, table, lens) -> lowram_pages:
+    """Descriptor of a paged 8-bit cache: codes [n_pages][H][page_tokens][d] (uint8 or e4m3),
+    scales [n_pages][H] fp32, table [n_seqs][max_pages] and lens [n_seqs] int32. It keeps
+    references to the tensors; lens and table are read on the device by every call, so they
+    may be updated in place between calls."""
+    import torch
+    if k_code.dim() != 4 or k_code.shape != v_code.shape:
+        raise ValueError("k_code and v_code must be [n_pages][H][page_tokens][d]")
+    if k_scale.shape != k_code.shape[:2] or v_scale.shape != k_code.shape[:2]:
+        raise ValueError("k_scale and v_scale must be [n_pages][H]")
+    if table.dim() != 2 or lens.shape != table.shape[:1]:
+        raise ValueError("table must be [n_seqs][max_pages] and lens [n_seqs]")
+    want = {"k_code": (k_code, (torch.uint8, torch.float8_e4m3fn)),
+            "v_code": (v_code, (torch.uint8, torch.float8_e4m3fn)),
+            "k_scale": (k_scale, (torch.float32,)), "v_scale": (v_scale, (torch.float32,)),
+            "table": (table, (torch.int32,)), "lens": (lens, (torch.int32,))}
+    for name, (t, dts) in want.items():
+        if t.dtype not in dts:
+            raise ValueError(f"{name} has dtype {t.dtype}")
+        if t.device != k_code.device:
+            raise ValueError(f"{name} is on {t.device}, k_code on {k_code.device}")
+    p = lowram_pages(_ptr(k_code), _ptr(v_code), _ptr(k_scale), _ptr(v_scale), _ptr(table),
+                     _ptr(lens), table.shape[0], table.shape[1], k_code.shape[0],
+                     k_code.shape[2])
+    p._refs = (k_code, v_code, k_scale, v_scale, table, lens)
+    p._ref = ctypes.byref(p)
+    p._heads = (k_code.shape[1], k_code.shape[3])
+    return p
+
+
+def _paged_check(ctx: Context, pages: lowram_pages, *tensors) -> None:
+    """The pages fit the context, and every tensor lies on its device."""
+    cfg = ctx.cfg
+    if pages._heads != (cfg.n_kv_heads, cfg.head_dim):
+        raise ValueError(f"pages of (heads, d) {pages._heads} in a context of "
+                         f"{(cfg.n_kv_heads, cfg.head_dim)}")
+    for t in (pages._refs[0],) + tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != ctx.device):
+            raise ValueError(f"tensor on {t.device}, context on cuda:{ctx.device}")
+
+
+def _paged_stream(ctx: Context, stream):
+    """The given stream, or the current one of the context's device."""
+    import torch
+    s = stream if stream is not None else torch.cuda.current_stream(ctx.device)
+    return s.cuda_stream
+
+
+def _float_dtype(ctx: Context):
+    import torch
+    return torch.bfloat16 if ctx.cfg.dtype == DTYPE_BF16 else torch.float32
+
+
+def _int32(t, n: int, name: str):
+    """Device address of an optional [n] int32 array."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or tuple(t.shape) != (n,):
+        raise ValueError(f"{name} must be int32 of shape ({n},), got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, max_new=None,
+                 pos_base=None, rotate: bool = True, stream=None) -> None:
+    """lowram_paged_append: k_new, v_new [n_new][H][d] (or [n_seqs][n][H][d], dense) are
+    appended to the pages, the keys rotated by their positions. The tokens of a 3-dimensional
+    k_new / v_new may lie any multiple of 16 bytes apart (slices of a fused projection).
+    pages' lens count the new tokens. cu_new [n_seqs + 1] int32 for ragged counts (max_new:
+    the largest, default n_new)."""
+    cfg = ctx.cfg
+    _paged_check(ctx, pages, k_new, v_new, cu_new, pos_base)
+    H, d = cfg.n_kv_heads, cfg.head_dim
+    dt = _float_dtype(ctx)
+    if k_new.shape != v_new.shape or k_new.dim() not in (3, 4) or k_new.shape[-2:] != (H, d):
+        raise ValueError(f"k_new and v_new must be [n_new][{H}][{d}]")
+    if k_new.dim() == 4:
+        if k_new.shape[0] != pages.n_seqs:
+            raise ValueError(f"k_new holds {k_new.shape[0]} sequences, the pages {pages.n_seqs}")
+        _ptr(k_new), _ptr(v_new)    # contiguity check
+        k_new, v_new = k_new.flatten(0, 1), v_new.flatten(0, 1)
+    n = k_new.shape[0]
+    strides = []
+    for t in (k_new, v_new):
+        st = t.stride()
+        if t.dtype != dt:
+            raise ValueError(f"k_new and v_new must be {dt}")
+        if n and (st[2] != 1 or (st[1] != d and H > 1)):
+            raise ValueError("the heads of a token must be dense")
+        strides.append(st[0] if n > 1 else H * d)
+    cu = _int32(cu_new, pages.n_seqs + 1, "cu_new")
+    check(lowram_paged_append(ctx.handle, pages._ref, k_new.data_ptr(), v_new.data_ptr(),
+                              strides[0], strides[1], n, cu, n if max_new is None else max_new,
+                              _int32(pos_base, pages.n_seqs, "pos_base"), 1 if rotate else 0,
+                              _paged_stream(ctx, stream)), "lowram_paged_append")
+
+
+def paged_workspace_size(cfg: lowram_config, n_seqs: int, n_q: int = 1) -> int:
+    n = ctypes.c_size_t()
+    check(lowram_paged_workspace_size(ctypes.byref(cfg), n_seqs, n_q, ctypes.byref(n)),
+          "lowram_paged_workspace_size")
+    return n.value
+
+
+def paged_attend(ctx: Context, pages: lowram_pages, q, out, workspace, lse=None,
+                 stream=None) -> None:
+    """lowram_paged_attend: attention of q [n_seqs][n_q][H_q][d] (or [n_seqs][H_q][d]: one
+    query a sequence) over the pages; out like q, lse [n_seqs][n_q][H_q] fp32."""
+    import torch
+    cfg = ctx.cfg
+    _paged_check(ctx, pages, q, out, workspace, lse)
+    dt = _float_dtype(ctx)
+    shape = q.shape
+    if (len(shape) not in (3, 4) or shape[0] != pages.n_seqs or shape[-2] != cfg.n_q_heads or
+            shape[-1] != cfg.head_dim or out.shape != shape):
+        raise ValueError(f"q and out must be [{pages.n_seqs}][n_q][{cfg.n_q_heads}]"
+                         f"[{cfg.head_dim}]")
+    if q.dtype != dt or out.dtype != dt:
+        raise ValueError(f"q and out must be {dt}")
+    n_q = shape[1] if len(shape) == 4 else 1
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1]):
+        raise ValueError(f"lse must be fp32 of shape {tuple(shape[:-1])}")
+    check(lowram_paged_attend(ctx.handle, pages._ref, _ptr(q), n_q, _ptr(out), _ptr(lse),
+                              _ptr(workspace), workspace.numel() * workspace.element_size(),
+                              _paged_stream(ctx, stream)), "lowram_paged_attend")
+
+
+def paged_gather(ctx: Context, pages: lowram_pages, k_out, v_out, start=None,
+                 stream=None) -> None:
+    """lowram_paged_gather: tokens start[b] .. of every sequence (default 0) read out of the
+    pages into k_out, v_out [n_seqs][n][H][d]; zeros outside the sequence."""
+    cfg = ctx.cfg
+    _paged_check(ctx, pages, k_out, v_out, start)
+    shape = k_out.shape
+    if (len(shape) != 4 or shape[0] != pages.n_seqs or
+            tuple(shape[2:]) != (cfg.n_kv_heads, cfg.head_dim) or v_out.shape != shape):
+        raise ValueError(f"k_out and v_out must be [{pages.n_seqs}][n][{cfg.n_kv_heads}]"
+                         f"[{cfg.head_dim}]")
+    if k_out.dtype != _float_dtype(ctx) or v_out.dtype != _float_dtype(ctx):
+        raise ValueError(f"k_out and v_out must be {_float_dtype(ctx)}")
+    check(lowram_paged_gather(ctx.handle, pages._ref, _int32(start, pages.n_seqs, "start"),
+                              shape[1], _ptr(k_out), _ptr(v_out), _paged_stream(ctx, stream)),
+          "lowram_paged_gather")
