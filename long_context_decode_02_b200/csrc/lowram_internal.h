@@ -237,7 +237,8 @@ cudaError_t launch_paged_gather(const PagedArgs& a, int num_sms, cudaStream_t s)
 size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q);
 cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s);
 
-// 2D tiled TMA map over a row-major [rows][cols] array of dtype (LOWRAM_DTYPE_*), box
+constexpr int kMapBytes = 100;   // make_tensor_map_2d's dtype of single bytes
+// 2D tiled TMA map over a row-major [rows][cols] array of dtype (LOWRAM_DTYPE_*, kMapBytes), box
 // box_rows x box_cols, swizzle 0/32/64/128 bytes; L2 fetches promoted to l2_promo bytes
 // (128 or 256). False if the driver refuses it.
 bool make_tensor_map_2d(CUtensorMap* m, const void* ptr, int dtype, uint64_t cols,

@@ -32,9 +32,10 @@ bool make_tensor_map_2d(CUtensorMap* m, const void* ptr, int dtype, uint64_t col
                         int l2_promo) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const size_t es = dtype == LOWRAM_DTYPE_BF16 ? 2 : 4;
-  const CUtensorMapDataType dt =
-      dtype == LOWRAM_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  const size_t es = dtype == kMapBytes ? 1 : dtype == LOWRAM_DTYPE_BF16 ? 2 : 4;
+  const CUtensorMapDataType dt = dtype == kMapBytes              ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                 : dtype == LOWRAM_DTYPE_BF16    ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_NONE;
   if (swizzle_bytes == 32) sw = CU_TENSOR_MAP_SWIZZLE_32B;
   else if (swizzle_bytes == 64) sw = CU_TENSOR_MAP_SWIZZLE_64B;

@@ -215,6 +215,29 @@ def test_attend_nan_only_reaches_its_rows(L):
     ctx.close()
 
 
+def test_attend_nan_value_of_a_drafted_token(L):
+    """A NaN value of a token that only the later queries see stays out of the earlier ones."""
+    for dtype, d, P in (("bf16", 128, 16), ("bf16", 64, 32), ("f32", 64, 16), ("f32", 128, 64)):
+        c = Case(L, [36, 50], P, 1, d, seed=14)
+        c.ref.code["v"][c.table[0, 34 // P], 0, 34 % P, 5] = 0xff
+        c.ref.code["v"][c.table[0, 35 // P], 0, 35 % P, 8] = 0x7f
+        pages = c.device()
+        ctx = context(L, dtype, 1, 2, d)
+        q = torch.randn(2, 4, 2, d, generator=torch.Generator().manual_seed(3)).to(DT[dtype]).cuda()
+        out = torch.empty_like(q)
+        ws = torch.empty(L.paged_workspace_size(ctx.cfg, 2, 4), dtype=torch.uint8, device="cuda")
+        L.paged_attend(ctx, pages, q, out, ws)
+        assert ctx.last_error() == L.OK
+        nan = torch.isnan(out).cpu()
+        want = torch.zeros_like(nan)
+        want[0, 2:, :, 5] = True
+        want[0, 3:, :, 8] = True
+        assert torch.equal(nan, want), (dtype, d)
+        ref = c.ref.attend(c.table, c.lens, f64(q), 2)
+        check_attend(dtype, out[:, :2], None, tuple(x[:, :2] for x in ref))
+        ctx.close()
+
+
 def check_append(c, wrote, t, base, d):
     """Codes and scales on the device against the reference, and untouched bytes."""
     for name, code, scale in (("k", t[0], t[2]), ("v", t[1], t[3])):
