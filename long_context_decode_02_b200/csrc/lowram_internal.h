@@ -234,7 +234,7 @@ struct PagedArgs {
 };
 cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedArgs& a, int num_sms, cudaStream_t s);
-size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q);
+size_t paged_attend_workspace_bytes(int H, int G, int d, int n_seqs, int n_q);
 cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s);
 
 constexpr int kMapBytes = 100;   // make_tensor_map_2d's dtype of single bytes
