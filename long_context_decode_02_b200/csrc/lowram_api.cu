@@ -899,7 +899,7 @@ lowram_status lowram_paged_workspace_size(const lowram_config* c, int32_t n_seqs
   if (n_seqs < 1 || n_q < 1) return LOWRAM_ERR_SHAPE;
   if (n_seqs > kPagedMaxSeqs || n_q > kPagedMaxQueries) return LOWRAM_ERR_UNSUPPORTED;
   *bytes = paged_attend_workspace_bytes(c->n_kv_heads, c->n_q_heads / c->n_kv_heads, c->head_dim,
-                                        n_seqs, n_q);
+                                        c->dtype, n_seqs, n_q);
   return LOWRAM_OK;
 }
 
@@ -922,7 +922,7 @@ lowram_status lowram_paged_attend(lowram_ctx* ctx, const lowram_pages* pages, co
   a.out = out;
   a.lse = lse;
   a.n_q = n_q;
-  a.ws = static_cast<float*>(workspace);
+  a.ws = workspace;
   if (launch_paged_attend(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return LOWRAM_ERR_CUDA;

@@ -228,13 +228,13 @@ struct PagedArgs {
   const int32_t* pos_base;        // or null
   // attend
   const void* q; void* out; float* lse; int n_q;
-  float* ws;
+  void* ws;
   // gather
   const int32_t* start; int n; void* k_out; void* v_out;
 };
 cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedArgs& a, int num_sms, cudaStream_t s);
-size_t paged_attend_workspace_bytes(int H, int G, int d, int n_seqs, int n_q);
+size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q);
 cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s);
 
 constexpr int kMapBytes = 100;   // make_tensor_map_2d's dtype of single bytes

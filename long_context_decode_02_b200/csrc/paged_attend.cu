@@ -2,12 +2,18 @@
 //   z_t = (q . k_code_t) k_scale / sqrt(d),  out = sum_t softmax(z)_t v_code_t v_scale.
 //
 // Bound by bytes: each code is read once (2 sum(len) H d bytes), for 4 G n_q operations a pair
-// of codes. The work is cut into steps of 32 tokens of one (sequence, KV head, group of query
-// rows); all steps in one list, an equal run of them for every warp of the GPU, so ragged
-// batches and single long sequences fill it alike. A warp streams its run alone: it issues TMA
-// boxes of 16 tokens into its own ring of stages, holds the queries as matrix fragments in
-// registers, and writes one partial (reference, sum, output) for every (sequence, head, group)
-// that its run touches. A second kernel merges the partials of a row.
+// of codes. The work is cut into steps of 8 KB (32 tokens, 64 for d = 64) of one (sequence, KV
+// head, group of query rows), all in one list, an equal run of them for every warp of the GPU, so
+// ragged batches and single long sequences fill it alike. A warp streams its run alone: it issues
+// TMA boxes into its own ring of stages, holds the queries as matrix fragments in registers, and
+// writes one partial (reference, sum, output) for every (sequence, head, group) that its run
+// touches. A second kernel merges the partials of a row.
+//
+// Two stages a warp, not three: with 192 KB of an SM always asked for, four groups of ten SMs get
+// a tenth less of the bandwidth than the others and end that much later (batch 8 at 128K tokens:
+// SMs end at 280 .. 350 us); with 128 KB all get the same (300 .. 319 us; the call 354 -> 326 us).
+// Handing the list's end out in short runs instead cost more than it evened out (a run's queries,
+// partial and pages are about 3 us of a warp).
 //
 // Matrix form, m16n8k16 with fp16 operands and fp32 sums: S^T = K Q^T (rows: 16 tokens) and
 // O^T += V^T P^T (rows: 16 elements of d), so the few query rows of a KV head fill the narrow side
@@ -39,43 +45,44 @@ namespace {
 using namespace sm100;
 
 constexpr int kWarps = 8;
-constexpr int kStep = 32;                 // tokens of a step: two units
-constexpr int kUnit = 16;
+constexpr int kUnit = 16;                 // tokens of a matrix tile
 constexpr int kMetaUnits = 64;            // a warp's ring of units' scales
 constexpr int kMaxCtas = 160;             // bound of the workspace; the grid is one CTA an SM
-constexpr uint32_t kRingBytes = 24 * 1024;   // a warp's ring
+constexpr int kStages = 2;                // a warp's ring: 16 KB
+constexpr uint32_t kHalfBytes = 4096;     // K (or V) of a step
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr uint32_t kRingBytes = kStages * kStageBytes;
 constexpr float kWeightScale = 8192.f;    // 2^13: weights in fp16 stay normal down to 2^-27
-constexpr int kCombineThreads = 128;
+constexpr int kCombineThreads = 256;
 
 template <int D> struct Tile {
-  static constexpr uint32_t kHalf = kStep * D;          // bytes of K (or V) of a step
-  static constexpr uint32_t kStage = 2 * kHalf;
-  static constexpr int kStages = kRingBytes / kStage;   // 3 (d = 128), 6 (d = 64)
+  static constexpr int kStep = kHalfBytes / D;       // tokens of a step: 32 (d = 128), 64
+  static constexpr int kUnits = kStep / kUnit;       // 2, 4
 };
 
 struct AttendMaps {
-  CUtensorMap k;   // [n_pages * H * page_tokens rows][d] bytes, box d x min(page_tokens, 32),
+  CUtensorMap k;   // [n_pages * H * page_tokens rows][d] bytes, box d x min(page_tokens, step),
                    // swizzled by d bytes
   CUtensorMap v;
 };
 
 // Query rows of one (sequence, KV head): r = j G + g, in groups of `rows`.
 struct RowPlan {
-  int rows, groups;   // rows of a group (4 or 8), groups
+  int rows, groups;   // rows of a group (4, 8; bf16: 16), groups
 };
-inline RowPlan row_plan(int G, int n_q) {
+inline RowPlan row_plan(int G, int n_q, int dtype) {
   const int R = G * n_q;
   RowPlan p;
-  p.rows = R <= 4 ? 4 : 8;
+  p.rows = R <= 4 ? 4 : R <= 8 || dtype != LOWRAM_DTYPE_BF16 ? 8 : 16;
   p.groups = (R + p.rows - 1) / p.rows;
   return p;
 }
 
-// Workspace: plan { share, prefix[n_seqs + 1] } in steps, then the partials' (m, l) and outputs.
-// The partial of warp w for pair x (= (b H + h) groups + group) is number w + x: both only grow
-// along the list of steps.
+// Workspace: first step of every sequence (of one pair each) and their total, for the merge of
+// more than 32 sequences; the partials' (m, l) and outputs. The partial of warp w for pair x (= (b H + h)
+// groups + group) is number w + x: both only grow along the list of steps.
 struct AttendWs {
-  long long* plan;
+  long long* first;   // [n_seqs + 1]
   float2* ml;   // [slots][rows]
   float* o;     // [slots][rows][d]
 };
@@ -83,10 +90,9 @@ inline size_t ws_align(size_t x) { return (x + 255) / 256 * 256; }
 inline AttendWs ws_layout(void* ws, int H, const RowPlan& rp, int d, int n_seqs, size_t* total) {
   uint8_t* p = static_cast<uint8_t*>(ws);
   const size_t slots = (size_t)kMaxCtas * kWarps + (size_t)n_seqs * H * rp.groups;
-  size_t o = 0;
   AttendWs w;
-  w.plan = reinterpret_cast<long long*>(p + o);
-  o = ws_align(o + (size_t)(n_seqs + 2) * sizeof(long long));
+  w.first = reinterpret_cast<long long*>(p);
+  size_t o = ws_align((size_t)(n_seqs + 1) * sizeof(long long));
   w.ml = reinterpret_cast<float2*>(p + o);
   o = ws_align(o + slots * rp.rows * sizeof(float2));
   w.o = reinterpret_cast<float*>(p + o);
@@ -99,8 +105,20 @@ struct AttendParams {
   PagedArgs a;
   RowPlan rp;
   AttendWs ws;
+  int n_warps;   // of the attend kernel
 };
 
+// Steps of a warp's run, of `total` in the list.
+__device__ __forceinline__ long long run_steps(long long total, int n_warps) {
+  return total > 0 ? (total + n_warps - 1) / n_warps : 1;
+}
+
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -156,177 +174,227 @@ template <int D> __device__ __forceinline__ uint32_t chunk_offset(int row, int c
   return D == 128 ? sw128_offset(row, c) : sw64_offset(row, c);
 }
 
-// RL: query rows of a lane, RL * 4 of a group. Columns 2 t, 2 t + 1 of a tile are, in fp32, the
-// high and low parts of row 4 x + t (tile x); in bf16 row t and nothing (RL = 1) or rows 2 t, 2 t + 1.
+// RL: query rows of a lane, 4 RL of a group. Columns 2 t, 2 t + 1 of a tile are, in fp32, the
+// high and low parts of row 4 x + t (tile x); in bf16 row t and nothing (RL = 1), or rows
+// 8 x + 2 t, 8 x + 2 t + 1 (tile x).
 template <typename T, int D, int RL, bool F32>
 __global__ void __launch_bounds__(kWarps * 32, 1)
 paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps maps) {
   using TL = Tile<D>;
-  constexpr int S = TL::kStages, kC = D / 16, kOT = D / 16;   // 16-byte chunks of a row
-  constexpr int NT = F32 ? RL : 1;          // column tiles
+  constexpr int S = kStages, U = TL::kUnits, kStep = TL::kStep;
+  constexpr int kC = D / 16, kOT = D / 16;          // 16-byte chunks of a row
+  constexpr int NT = F32 ? RL : (RL + 1) / 2;       // column tiles
   extern __shared__ uint8_t smem_raw[];
   __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, fr 2^13, ev, valid tokens
+  __shared__ int4 s_desc[kWarps][S];        // a stage's step: sequence, pair, first token, length
+  __shared__ int2 s_part[kWarps][S];        // its partial; 1: begins one, 2: ends it
   __shared__ int s_nan[kWarps][D];          // first token with a NaN value that not all rows see
   __shared__ alignas(8) uint64_t s_bar[kWarps][S];
   __shared__ int s_abort;
   const PagedArgs& a = p.a;
   const lowram_pages& pg = a.pg;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int P = pg.page_tokens, upp = P / kUnit;      // 16-token units of a page: 1, 2, 4
-  const int lgu = 31 - __clz(upp);
+  const int P = pg.page_tokens, lgu = 31 - __clz(P / kUnit);   // log2 units of a page: 0, 1, 2
   const int pairs = a.H * p.rp.groups;                // of one sequence
   const int R = a.G * a.n_q;
   const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + warp * kRingBytes;
   if (threadIdx.x == 0) s_abort = 0;
   if (lane == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 2);
+    for (int i = 0; i < S; ++i) mbar_init(smem_u32(&s_bar[warp][i]), U);
     fence_mbar_init();
   }
   __syncthreads();
+  grid_launch_dependents();   // the merge may be set up; it waits for this grid's end
   volatile int* abort_flag = &s_abort;
 
-  // ---- this warp's run of steps
+  // ---- the list of steps
+  auto steps_of = [&](int n) { return (n + kStep - 1) / kStep; };
+  auto scan = [&](int x) {   // inclusive, over the lanes
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  const int len0 = lane < pg.n_seqs ? paged_len(pg, lane, a.status) : 0;
+  auto len_at = [&](int b) {   // b = lane + 32 i
+    return b < 32 ? len0 : b < pg.n_seqs ? paged_len(pg, b, nullptr) : 0;
+  };
   long long total = 0;
   for (int b0 = 0; b0 < pg.n_seqs; b0 += 32) {
     const int b = b0 + lane;
-    int n = b < pg.n_seqs ? (paged_len(pg, b, a.status) + kStep - 1) / kStep : 0;
-    n = __reduce_add_sync(0xffffffffu, n);
-    total += n;
+    const int n = b < 32 ? len0 : b < pg.n_seqs ? paged_len(pg, b, a.status) : 0;
+    total += __reduce_add_sync(0xffffffffu, steps_of(n));
   }
-  total *= pairs;
-  const int n_warps = gridDim.x * kWarps;
-  // consecutive runs go to different SMs, so that little work still uses many of them
-  const int w = warp * gridDim.x + blockIdx.x;
-  const long long share = total > 0 ? (total + n_warps - 1) / n_warps : 1;
-  const long long w0 = min(total, w * share), w1 = min(total, w0 + share);
-  const int n_steps = (int)(w1 - w0);
-  if (w == 0) {   // the plan, for the merge
+  if (pg.n_seqs > 32 && warp == 0 && blockIdx.x == 0) {   // for the merge
     long long at = 0;
     for (int b0 = 0; b0 < pg.n_seqs; b0 += 32) {
-      const int b = b0 + lane;
-      const int n = b < pg.n_seqs ? (paged_len(pg, b, nullptr) + kStep - 1) / kStep : 0;
-      int x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (b < pg.n_seqs) p.ws.plan[1 + b] = (at + x - n) * pairs;
+      const int n = steps_of(len_at(b0 + lane)), x = scan(n);
+      if (b0 + lane < pg.n_seqs) p.ws.first[b0 + lane] = at + x - n;
       at += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) {
-      p.ws.plan[0] = share;
-      p.ws.plan[1 + pg.n_seqs] = total;
-    }
+    if (lane == 0) p.ws.first[pg.n_seqs] = total;
   }
-  if (n_steps == 0) return;
-  // where the run begins: sequence, pair, step
-  int b = 0, len = 0, ns = 0, pair = 0, step = 0;
-  {
+  total *= pairs;
+  // consecutive runs go to different SMs, so that little work still uses many of them
+  const int run = warp * gridDim.x + blockIdx.x;
+
+  // ---- the loader. It works in batches of up to 32 units (a lane each) of one pair, and looks
+  // up a batch's pages, then its scales, while the batch before is being issued.
+  constexpr int kBatch = 32 / U;     // steps of a batch
+  const uint32_t bar0 = smem_u32(&s_bar[warp][0]);
+  int lb = 0, llen = 0, lns = 1, lpair = 0, lstep = 0;   // cursor: behind the batch looked up last
+  int left = 0, flag = 1;            // steps left of the run; the next batch begins a partial
+  int nb = 0, npair = 0, ntok = 0, nlen = 0, ncnt = 0, nslot = 0, nflag = 0;   // next batch
+  int npage = -1, nvalid = 0;        // its unit of this lane: page, tokens, scales
+  float nsk = 0.f, nsv = 0.f;
+  bool nscaled = false;
+  int cb = 0, cpair = 0, ctok = 0, clen = 0, ccnt = 0, cslot = 0, cflag = 0;   // current batch
+  int uy = -1, off = 0;              // its unit of this lane: row of its box; the step's first unit
+  int lst = 0, issued = 0;
+  {   // where the run begins: sequence, pair, step
+    const long long steps = run_steps(total, p.n_warps);
+    const long long r0 = min(total, run * steps);
+    left = (int)(min(total, r0 + steps) - r0);
     long long at = 0;
-    for (int b0 = 0;; b0 += 32) {
-      const int bb = b0 + lane;
-      const int n = bb < pg.n_seqs ? paged_len(pg, bb, nullptr) : 0;
-      const int s = (n + kStep - 1) / kStep;
-      int x = s;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      const unsigned past = __ballot_sync(0xffffffffu, (at + x) * pairs > w0);
+    for (int b0 = 0; left > 0 && b0 < pg.n_seqs; b0 += 32) {
+      const int n = len_at(b0 + lane), x = scan(steps_of(n));
+      const unsigned past = __ballot_sync(0xffffffffu, (at + x) * pairs > r0);
       if (past) {
         const int src = __ffs(past) - 1;
-        b = b0 + src;
-        len = __shfl_sync(0xffffffffu, n, src);
-        ns = (len + kStep - 1) / kStep;
-        const long long off = w0 - (at + __shfl_sync(0xffffffffu, x, src) - ns) * pairs;
-        pair = (int)(off / ns);
-        step = (int)(off % ns);
+        lb = b0 + src;
+        llen = __shfl_sync(0xffffffffu, n, src);
+        lns = steps_of(llen);
+        const long long in = r0 - (at + __shfl_sync(0xffffffffu, x, src) - lns) * pairs;
+        lpair = (int)(in / lns);
+        lstep = (int)(in % lns);
         break;
       }
       at += __shfl_sync(0xffffffffu, x, 31);
     }
   }
-  // the loader's cursor runs ahead of the consumer's
-  auto next_seq = [&](int& bb, int& ll, int& nn) {
-    do {
-      ++bb;
-      ll = bb < pg.n_seqs ? paged_len(pg, bb, nullptr) : 0;
-      nn = (ll + kStep - 1) / kStep;
-    } while (nn == 0 && bb < pg.n_seqs);
-  };
-  int lb = b, llen = len, lns = ns, lpair = pair, lstep = step, lst = 0, issued = 0;
-  int off = 32;                      // the step's first unit among the lanes' page entries
-  int uy = -1;                       // this lane's unit: row of its box, -1 for none
-  const uint32_t bar0 = smem_u32(&s_bar[warp][0]);
-  auto issue = [&]() {
-    if (off + 2 > 32) {              // the next 32 units' pages and scales, a lane each
-      off = 0;
-      const int u = 2 * lstep + lane, h = lpair / p.rp.groups;
-      uy = -1;
-      float4 me = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (u * kUnit < llen) {
-        const int page = paged_page(pg, lb, u >> lgu, a.status);
-        if (page >= 0) {
-          const size_t ph = (size_t)page * a.H + h;
-          const float sk = pg.k_scale[ph], sv = pg.v_scale[ph];
-          uy = (int)ph * P + (u & (upp - 1)) * kUnit;
-          int ev = (int)((__float_as_uint(sv) >> 23) & 255u) - 127;
-          ev = min(max(ev, -64), 120);
-          me = make_float4(sk, sv * __int_as_float((127 - ev) << 23) * kWeightScale,
-                           __int_as_float(ev), __int_as_float(min(llen - u * kUnit, kUnit)));
-        }
-      }
-      s_meta[warp][(2 * issued + lane) & (kMetaUnits - 1)] = me;
-    }
-    const int mine = lane - off;
-    if (mine == 0 || mine == 1) {
-      const uint32_t bar = bar0 + 8u * lst;
-      const uint32_t dst = ring + lst * TL::kStage + mine * kUnit * D;
-      // both units of a step lie in one page of 32 or 64 tokens: one box
-      const bool load = uy >= 0 && (mine == 0 || upp == 1);
-      mbar_arrive_expect_tx(bar, load ? (upp == 1 ? 2 * kUnit * D : 2 * kStep * D) : 0);
-      if (load) {
-        tma_load_2d(dst, &maps.k, 0, uy, bar);
-        tma_load_2d(dst + TL::kHalf, &maps.v, 0, uy, bar);
-      }
-    }
-    off += 2;
-    ++issued;
-    if (++lst == S) lst = 0;
-    if (++lstep == lns) {
+  auto look_up = [&]() {             // the next batch: where it lies, and its pages
+    ncnt = 0;
+    if (left == 0) return;
+    nb = lb;
+    npair = lpair;
+    ntok = lstep * kStep;
+    nlen = llen;
+    ncnt = min(min(kBatch, lns - lstep), left);
+    nslot = run + lb * pairs + lpair;
+    const int u = U * lstep + lane;
+    nvalid = min(max(llen - u * kUnit, 0), kUnit);
+    if (lane >= U * ncnt) nvalid = 0;
+    npage = nvalid > 0 ? pg.table[(size_t)lb * pg.max_pages + (u >> lgu)] : -1;
+    nscaled = false;
+    lstep += ncnt;
+    left -= ncnt;
+    const bool ends = lstep == lns || left == 0;
+    nflag = flag | (ends ? 2 : 0);
+    flag = ends ? 1 : 0;
+    if (lstep == lns && left > 0) {
       lstep = 0;
-      off = 32;
       if (++lpair == pairs) {
         lpair = 0;
-        next_seq(lb, llen, lns);
+        do {
+          ++lb;
+          llen = lb >= pg.n_seqs ? 0 : lb < 32 ? __shfl_sync(0xffffffffu, len0, lb)
+                                               : paged_len(pg, lb, nullptr);
+          lns = steps_of(llen);
+        } while (lns == 0 && lb < pg.n_seqs);
       }
     }
   };
+  auto look_up_scales = [&]() {
+    nscaled = true;
+    if (nvalid > 0 && (npage < 0 || npage >= pg.n_pages)) {
+      raise_status(a.status, kStatusDeviceCheck);
+      nvalid = 0;
+    }
+    if (nvalid > 0) {
+      const size_t ph = (size_t)npage * a.H + npair / p.rp.groups;
+      nsk = pg.k_scale[ph];
+      nsv = pg.v_scale[ph];
+    }
+  };
+  auto issue = [&]() {
+    if (ccnt == 0) {                 // the next batch becomes the current one
+      if (!nscaled) look_up_scales();
+      cb = nb; cpair = npair; ctok = ntok; clen = nlen; ccnt = ncnt; cslot = nslot; cflag = nflag;
+      const int h = cpair / p.rp.groups;
+      const int u = ctok / kUnit + lane;
+      uy = nvalid > 0 ? (npage * a.H + h) * P + (u & ((1 << lgu) - 1)) * kUnit : -1;
+      off = 0;
+      int ev = (int)((__float_as_uint(nsv) >> 23) & 255u) - 127;
+      ev = min(max(ev, -64), 120);
+      s_meta[warp][(U * issued + lane) & (kMetaUnits - 1)] =
+          make_float4(nsk, nsv * __int_as_float((127 - ev) << 23) * kWeightScale,
+                      __int_as_float(ev), __int_as_float(nvalid));
+      look_up();
+    } else if (!nscaled) {
+      look_up_scales();
+    }
+    const int mine = lane - off;
+    if (mine >= 0 && mine < U) {
+      const uint32_t bar = bar0 + 8u * lst;
+      const uint32_t dst = ring + lst * kStageBytes + mine * kUnit * D;
+      // units of one page (and step) come as one box
+      const bool load = uy >= 0 && (mine & ((1 << lgu) - 1)) == 0;
+      mbar_arrive_expect_tx(bar, load ? 2 * min(P, kStep) * D : 0);
+      if (load) {
+        tma_load_2d(dst, &maps.k, 0, uy, bar);
+        tma_load_2d(dst + kHalfBytes, &maps.v, 0, uy, bar);
+      }
+    }
+    --ccnt;
+    if (lane == 0) {
+      s_desc[warp][lst] = make_int4(cb, cpair, ctok, clen);
+      s_part[warp][lst] = make_int2(cslot, ccnt == 0 ? cflag : cflag & 1);
+    }
+    cflag &= 2;                      // only the batch's first step begins a partial
+    ctok += kStep;
+    off += U;
+    ++issued;
+    if (++lst == S) lst = 0;
+    __syncwarp();
+  };
+  look_up();
 
   // ---- state of the current (sequence, head, group)
+  auto row_of = [&](int x) {        // this lane's x-th row of the group
+    return F32 ? 4 * x + t : RL == 1 ? t : 8 * (x >> 1) + 2 * t + (x & 1);
+  };
   uint32_t qf[NT][kC][2];
   float cs[RL];                     // logit of a row in log2 units per unit of S
   int lim[RL];                      // tokens that the row sees
   float m[RL], l[RL], O[NT][kOT][4];
   // the rows that this lane names to ldmatrix, in a step's K (a unit's) and V
-  const int krow = s_token(lane & 15), vrow = v_token(lane & 15) + (lane & 16);
-  bool fresh = true, good = true, poison = false;
+  const int krow = s_token(lane & 15), vrow = v_token(lane & 15) + (lane & 16);   // two units' V
+  bool good = true, poison = false;
   int landed = 0, st = 0, row0 = 0, vis = 0;   // vis: tokens that every row of the group sees
   uint32_t parity = 0;
-  for (int it = 0; it < n_steps + S; ++it) {
-    if (it >= S) {
-      if (fresh) {   // the group's queries
-        fresh = false;
-        const int h = pair / p.rp.groups;
-        row0 = (pair - h * p.rp.groups) * p.rp.rows;
+  for (;;) {
+    if (ccnt + ncnt > 0 && issued < landed + S) {
+      __syncwarp();   // every lane has read the stage (and its meta) that is filled again
+      issue();
+      if (ccnt + ncnt > 0 && issued < landed + S) continue;
+    }
+    if (landed == issued) break;
+    {
+      const int4 ds = s_desc[warp][st];   // sequence, pair, first token, length
+      const int2 part = s_part[warp][st];
+      const int tok0 = ds.z;
+      if (part.y & 1) {   // a new (sequence, head, group): its queries
+        const int b = ds.x, h = ds.y / p.rp.groups, len = ds.w;
+        poison = false;
+        row0 = (ds.y - h * p.rp.groups) * p.rp.rows;
         vis = len - a.n_q + row0 / a.G + 1;
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           // the row of this lane's column, if it has one
-          const int r = F32 ? row0 + 4 * x + (g >> 1) : RL == 1 ? row0 + (g >> 1) : row0 + g;
-          const bool has = r < R && (F32 || RL == 2 || (g & 1) == 0);
+          const int r = row0 + (F32 ? 4 * x + (g >> 1) : RL == 1 ? g >> 1 : 8 * x + g);
+          const bool has = r < R && (F32 || RL > 1 || (g & 1) == 0);
           float q[kC][4], top = 0.f;
 #pragma unroll
           for (int c = 0; c < kC; ++c)
@@ -361,7 +429,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
                               (1.4426950408889634f * rsqrtf((float)D));
 #pragma unroll
           for (int y = 0; y < RL; ++y)
-            if (!F32 || x == y) cs[y] = __shfl_sync(0xffffffffu, scale, 8 * t + (F32 ? 0 : 4 * y));
+            if (x == (F32 ? y : y >> 1))
+              cs[y] = __shfl_sync(0xffffffffu, scale, 8 * t + (F32 ? 0 : 4 * (y & 1)));
 #pragma unroll
           for (int j = 0; j < kOT; ++j)
 #pragma unroll
@@ -369,7 +438,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         }
 #pragma unroll
         for (int x = 0; x < RL; ++x) {
-          const int r = row0 + (F32 ? 4 * x + t : RL * t + x);
+          const int r = row0 + row_of(x);
           lim[x] = r < R ? len - a.n_q + r / a.G + 1 : 0;
           m[x] = -INFINITY;
           l[x] = 0.f;
@@ -378,20 +447,19 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
       good = mbar_wait_bounded(bar0 + 8u * st, parity, abort_flag);
       good = __all_sync(0xffffffffu, good);
       if (!good) break;
-      const uint32_t kb = ring + st * TL::kStage, vb = kb + TL::kHalf;
-      const float4* meta = &s_meta[warp][(2 * landed) & (kMetaUnits - 1)];   // an even slot
-      const float4 me[2] = {meta[0], meta[1]};
-      const int valid[2] = {__float_as_int(me[0].w), __float_as_int(me[1].w)};
+      const uint32_t kb = ring + st * kStageBytes, vb = kb + kHalfBytes;
+      const float4* meta = &s_meta[warp][(U * landed) & (kMetaUnits - 1)];   // a multiple of U
       ++landed;
       if (++st == S) {
         st = 0;
         parity ^= 1u;
       }
       // S^T = K Q^T: logits in log2 units, masked ones -inf; z[u][x][k]: token row g + 8 k
-      float z[2][RL][2];
+      float z[U][RL][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
+      for (int u = 0; u < U; ++u) {
         float c[2][NT][4];   // even and odd chunks
+        const float sk = meta[u].x;
 #pragma unroll
         for (int k = 0; k < kC; k += 2) {
           uint32_t r[4], f[4];
@@ -410,28 +478,32 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         for (int x = 0; x < RL; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int e = 2 * k + (!F32 && RL == 2 ? x : 0), nt = F32 ? x : 0;
+            const int e = 2 * k + (F32 ? 0 : x & 1), nt = F32 ? x : x >> 1;
             float v = c[0][nt][e] + c[1][nt][e];
             if (F32) v += c[0][nt][2 * k + 1] + c[1][nt][2 * k + 1];
-            z[u][x][k] = v * (cs[x] * me[u].x);
+            z[u][x][k] = v * (cs[x] * sk);
           }
       }
-      if (valid[0] < kUnit || valid[1] < kUnit || (step + 1) * kStep > vis) {
+      int least = kUnit;
+#pragma unroll
+      for (int u = 0; u < U; ++u) least = min(least, __float_as_int(meta[u].w));
+      if (least < kUnit || tok0 + kStep > vis) {
         // not every token of the step is seen by every row: masked logits, and V rows that are
         // no token (their bytes may be anything) set to zero
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
+          const int valid = __float_as_int(meta[u].w);
 #pragma unroll
           for (int x = 0; x < RL; ++x)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               const int tk = s_token(g + 8 * k);
-              if (tk >= valid[u] || step * kStep + u * kUnit + tk >= lim[x]) z[u][x][k] = -INFINITY;
+              if (tk >= valid || tok0 + u * kUnit + tk >= lim[x]) z[u][x][k] = -INFINITY;
             }
           for (int r = 0; r < kUnit; ++r) {
-            const int row = u * kUnit + r, tk = step * kStep + row;
+            const int row = u * kUnit + r, tk = tok0 + row;
             uint8_t* bytes = smem_raw + (vb - smem_u32(smem_raw)) + row * D;
-            if (r >= valid[u]) {
+            if (r >= valid) {
               if (lane < D / 4) reinterpret_cast<uint32_t*>(bytes)[lane] = 0;
             } else if (tk >= vis) {
               // a token that only some rows see: its NaN codes would reach the others as 0 * NaN,
@@ -460,12 +532,16 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         fence_proxy_async_smem();   // before a copy fills the stage again
       }
       // reference: max of z + ev
-      const float ev[2] = {(float)__float_as_int(me[0].z), (float)__float_as_int(me[1].z)};
+      float ev[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) ev[u] = (float)__float_as_int(meta[u].z);
       float mn[RL];
       bool grow = false;
 #pragma unroll
       for (int x = 0; x < RL; ++x) {
-        float v = fmaxf(fmaxf(z[0][x][0], z[0][x][1]) + ev[0], fmaxf(z[1][x][0], z[1][x][1]) + ev[1]);
+        float v = fmaxf(z[0][x][0], z[0][x][1]) + ev[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(z[u][x][0], z[u][x][1]) + ev[u]);
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
@@ -485,65 +561,72 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 #pragma unroll
           for (int j = 0; j < kOT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) O[x][j][e] *= corr[F32 ? x : RL == 1 ? 0 : e & 1];
+            for (int e = 0; e < 4; ++e) O[x][j][e] *= corr[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)];
       }
       // weights, as B operands of O^T += V^T P^T
-      uint32_t pf[2][NT][2];
+      uint32_t pf[U][NT][2];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float back = __int_as_float((127 - __float_as_int(me[u].z)) << 23);   // 2^-ev
+      for (int u = 0; u < U; ++u) {
+        const float back = __int_as_float((127 - __float_as_int(meta[u].z)) << 23);   // 2^-ev
+        const float sv = meta[u].y;
         float wgt[RL][2];
 #pragma unroll
         for (int x = 0; x < RL; ++x) {
           const float off = m[x] == -INFINITY ? 0.f : ev[u] - m[x];
           const float a0 = ex2_approx(z[u][x][0] + off), a1 = ex2_approx(z[u][x][1] + off);
           l[x] = fmaf(a0 + a1, back, l[x]);
-          wgt[x][0] = a0 * me[u].y;
-          wgt[x][1] = a1 * me[u].y;
+          wgt[x][0] = a0 * sv;
+          wgt[x][1] = a1 * sv;
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float hi = wgt[x][k];
-            const float lo = F32 ? hi - round_f16(hi) : RL == 2 ? wgt[RL - 1][k] : 0.f;
+            const float hi = wgt[F32 || RL == 1 ? x : 2 * x][k];
+            const float lo = F32 ? hi - round_f16(hi) : RL == 1 ? 0.f : wgt[RL == 1 ? 0 : 2 * x + 1][k];
             pf[u][x][k] = movmatrix_trans(pack_f16x2(hi, lo));
           }
       }
       // O^T += V^T P^T
 #pragma unroll
       for (int j = 0; j < kOT; ++j) {
-        uint32_t f[4], f0[4], f1[4];
-        ldmatrix_b8_trans(vb + chunk_offset<D>(vrow, j), f);   // elements 16 j ..
-        widen(f[0], f[1], f0);
-        widen(f[2], f[3], f1);
+        float o[NT][4];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          if (F32) {
-            float o[4];
-            mma_f16_first(o, f0, pf[0][x][0], pf[0][x][1]);
-            mma_f16(o, f1, pf[1][x][0], pf[1][x][1]);
+        for (int u = 0; u < U; u += 2) {
+          uint32_t f[4], f0[4], f1[4];
+          ldmatrix_b8_trans(vb + chunk_offset<D>(u * kUnit + vrow, j), f);   // elements 16 j ..
+          widen(f[0], f[1], f0);
+          widen(f[2], f[3], f1);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) O[x][j][e] += o[e];
-          } else {
-            mma_f16(O[x][j], f0, pf[0][x][0], pf[0][x][1]);
-            mma_f16(O[x][j], f1, pf[1][x][0], pf[1][x][1]);
+          for (int x = 0; x < NT; ++x) {
+            if (F32) {
+              if (u == 0) mma_f16_first(o[x], f0, pf[u][x][0], pf[u][x][1]);
+              else mma_f16(o[x], f0, pf[u][x][0], pf[u][x][1]);
+              mma_f16(o[x], f1, pf[u + 1][x][0], pf[u + 1][x][1]);
+            } else {
+              mma_f16(O[x][j], f0, pf[u][x][0], pf[u][x][1]);
+              mma_f16(O[x][j], f1, pf[u + 1][x][0], pf[u + 1][x][1]);
+            }
           }
+        }
+        if (F32) {
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[x][j][e] += o[x][e];
         }
       }
       // end of the pair, or of the run: its partial
-      const bool last = ++step == ns;
-      if (last || landed == n_steps) {
-        const size_t slot = (size_t)w + (size_t)b * pairs + pair;
-        float* po = p.ws.o + slot * p.rp.rows * D;
-        float2* pml = p.ws.ml + slot * p.rp.rows;
+      if (part.y & 2) {
+        float* po = p.ws.o + (size_t)part.x * p.rp.rows * D;
+        float2* pml = p.ws.ml + (size_t)part.x * p.rp.rows;
 #pragma unroll
         for (int x = 0; x < RL; ++x) {
           float v = l[x];
           v += __shfl_xor_sync(0xffffffffu, v, 4);
           v += __shfl_xor_sync(0xffffffffu, v, 8);
           v += __shfl_xor_sync(0xffffffffu, v, 16);
-          const int r = F32 ? 4 * x + t : RL * t + x;   // row of the group
+          const int r = row_of(x);
           if (row0 + r < R) {
             if (g == 0) pml[r] = make_float2(m[x], v);
 #pragma unroll
@@ -552,25 +635,14 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
               for (int k = 0; k < 2; ++k) {
                 const int el = 16 * j + g + 8 * k;
                 float o = F32 ? O[F32 ? x : 0][j][2 * k] + O[F32 ? x : 0][j][2 * k + 1]
-                              : O[0][j][2 * k + (RL == 2 ? x : 0)];
+                              : O[x >> 1][j][2 * k + (x & 1)];
                 if (poison && s_nan[warp][el] < lim[x]) o = __int_as_float(0x7fffffff);
                 po[(size_t)r * D + el] = o;
               }
           }
         }
-        fresh = true;
-        poison = false;
-        if (last) {
-          step = 0;
-          if (++pair == pairs) {
-            pair = 0;
-            next_seq(b, len, ns);
-          }
-        }
       }
     }
-    __syncwarp();   // every lane has read the stage (and its meta) that is filled again
-    if (it < n_steps) issue();
   }
   if (!good) {   // a wait gave up: the copies still in flight land first
     if (lane == 0) raise_status(a.status, kStatusTimeout);
@@ -586,38 +658,47 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 }
 
 // One CTA a query row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the partials
-// of its pair; the warps take every fourth partial.
+// of its pair. The warps take every eighth partial with a running maximum each, so that all of a
+// row's loads are in flight together. Where the partials lie follows from the lengths; up to 32
+// sequences it is worked out while the first kernel runs.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const AttendParams p) {
-  constexpr int E = D / 32, kW = kCombineThreads / 32;
+  constexpr int E = D / 32, kW = kCombineThreads / 32, kStep = Tile<D>::kStep;
   const PagedArgs& a = p.a;
+  const lowram_pages& pg = a.pg;
   const int hq = blockIdx.x % a.Hq, j = blockIdx.x / a.Hq, b = blockIdx.y;
   const int h = hq / a.G, r = j * a.G + hq % a.G;
   const int grp = r / p.rp.rows, rg = r % p.rp.rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = a.H * p.rp.groups, pair = h * p.rp.groups + grp;
-  const long long share = p.ws.plan[0];
-  const long long begin = p.ws.plan[1 + b], ns = (p.ws.plan[2 + b] - begin) / pairs;
-  const size_t row = ((size_t)b * a.n_q + j) * a.Hq + hq;
-  const long long s0 = begin + pair * ns;
+  long long total, before;
+  int ns;
+  if (pg.n_seqs <= 32) {
+    const int n = lane < pg.n_seqs ? (paged_len(pg, lane, nullptr) + kStep - 1) / kStep : 0;
+    total = __reduce_add_sync(0xffffffffu, n);
+    before = __reduce_add_sync(0xffffffffu, lane < b ? n : 0);
+    ns = __shfl_sync(0xffffffffu, n, b);
+  } else {
+    grid_dependency_wait();
+    total = p.ws.first[pg.n_seqs];
+    before = p.ws.first[b];
+    ns = (int)(p.ws.first[b + 1] - before);
+  }
+  const long long share = run_steps(total * pairs, p.n_warps);
+  const long long s0 = before * pairs + (long long)pair * ns;
   const int first = (int)(s0 / share);
   const int count = ns > 0 ? (int)((s0 + ns - 1) / share) - first + 1 : 0;
   const size_t slot0 = (size_t)first + (size_t)b * pairs + pair;
   const float2* ml = p.ws.ml + slot0 * p.rp.rows + rg;
   const float* po = p.ws.o + (slot0 * p.rp.rows + rg) * D + lane * E;
   const size_t so = (size_t)p.rp.rows * D;
-  float M = -INFINITY;
-  for (int s = lane; s < count; s += 32) M = fmaxf(M, ml[(size_t)s * p.rp.rows].x);
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[E];
+  const size_t row = ((size_t)b * a.n_q + j) * a.Hq + hq;
+  grid_dependency_wait();
+  float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
   for (int s = warp; s < count; s += kW) {
     const float2 x = ml[(size_t)s * p.rp.rows];
-    // a partial that saw nothing holds zeros; a NaN sum must stay one
-    const float c = x.x == -INFINITY ? (x.y == 0.f ? 0.f : 1.f) : exp2f(x.x - M);
-    L = fmaf(c, x.y, L);
     float o[E];
     if constexpr (E == 4) {
       const float4 y = *reinterpret_cast<const float4*>(po + s * so);
@@ -626,34 +707,48 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
       const float2 y = *reinterpret_cast<const float2*>(po + s * so);
       o[0] = y.x; o[1] = y.y;
     }
+    const float mn = fmaxf(m, x.x);
+    // a partial that saw nothing holds zeros; a NaN sum must stay one
+    const float c = m == -INFINITY ? 1.f : exp2f(m - mn);
+    const float w = x.x == -INFINITY ? 1.f : exp2f(x.x - mn);
+    m = mn;
+    l = fmaf(l, c, w * x.y);
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(c, o[e], acc[e]);
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], c, w * o[e]);
   }
-  __shared__ float s_l[kW], s_o[kW][D];
-  if (lane == 0) s_l[warp] = L;
+  __shared__ float s_m[kW], s_l[kW], s_o[kW][D];
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
 #pragma unroll
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = acc[e];
   __syncthreads();
-  L = 0.f;
+  float M = -INFINITY, L = 0.f, w[kW];
 #pragma unroll
-  for (int x = 0; x < kW; ++x) L += s_l[x];
+  for (int x = 0; x < kW; ++x) M = fmaxf(M, s_m[x]);
+#pragma unroll
+  for (int x = 0; x < kW; ++x) {
+    w[x] = s_m[x] == -INFINITY ? 1.f : exp2f(s_m[x] - M);
+    L = fmaf(w[x], s_l[x], L);
+  }
   const float inv = L == 0.f ? 0.f : 1.f / (L * kWeightScale);
-  for (int e = threadIdx.x; e < D; e += kCombineThreads) {
+  if (threadIdx.x < D) {
     float o = 0.f;
 #pragma unroll
-    for (int x = 0; x < kW; ++x) o += s_o[x][e];
-    ((T*)a.out)[row * D + e] = from_f<T>(o * inv);
+    for (int x = 0; x < kW; ++x) o = fmaf(w[x], s_o[x][threadIdx.x], o);
+    ((T*)a.out)[row * D + threadIdx.x] = from_f<T>(o * inv);
   }
   if (a.lse && threadIdx.x == 0)
     a.lse[row] = L == 0.f ? -INFINITY : fmaf(M, 0.69314718055994531f, logf(L));
 }
 
 template <typename T, int D, int RL, bool F32>
-cudaError_t attend_t(const AttendParams& p, int num_sms, cudaStream_t s) {
+cudaError_t attend_t(const AttendParams& p, cudaStream_t s) {
   const PagedArgs& a = p.a;
   AttendMaps maps;
   const uint64_t rows = (uint64_t)a.pg.n_pages * a.H * a.pg.page_tokens;
-  const uint32_t box = a.pg.page_tokens < kStep ? kUnit : kStep;
+  const uint32_t box = a.pg.page_tokens < Tile<D>::kStep ? a.pg.page_tokens : Tile<D>::kStep;
   if (!make_tensor_map_2d(&maps.k, a.pg.k_code, kMapBytes, D, rows, D, box, D, 256) ||
       !make_tensor_map_2d(&maps.v, a.pg.v_code, kMapBytes, D, rows, D, box, D, 256))
     return cudaErrorInvalidValue;
@@ -661,36 +756,48 @@ cudaError_t attend_t(const AttendParams& p, int num_sms, cudaStream_t s) {
   auto kern = paged_attend_kernel<T, D, RL, F32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<num_sms < kMaxCtas ? num_sms : kMaxCtas, kWarps * 32, smem, s>>>(p, maps);
+  kern<<<p.n_warps / kWarps, kWarps * 32, smem, s>>>(p, maps);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  paged_combine_kernel<T, D><<<dim3(a.n_q * a.Hq, a.pg.n_seqs), kCombineThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  // set up while the first kernel runs
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(a.n_q * a.Hq, a.pg.n_seqs);
+  lc.blockDim = dim3(kCombineThreads);
+  lc.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, paged_combine_kernel<T, D>, p);
 }
 
 template <typename T, int D, bool F32>
-cudaError_t attend_d(const AttendParams& p, int num_sms, cudaStream_t s) {
-  return p.rp.rows == 4 ? attend_t<T, D, 1, F32>(p, num_sms, s)
-                        : attend_t<T, D, 2, F32>(p, num_sms, s);
+cudaError_t attend_d(const AttendParams& p, cudaStream_t s) {
+  if (p.rp.rows == 4) return attend_t<T, D, 1, F32>(p, s);
+  if constexpr (!F32)
+    if (p.rp.rows == 16) return attend_t<T, D, 4, F32>(p, s);
+  return attend_t<T, D, 2, F32>(p, s);
 }
 
 }  // namespace
 
-size_t paged_attend_workspace_bytes(int H, int G, int d, int n_seqs, int n_q) {
+size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q) {
   size_t total = 0;
-  ws_layout(nullptr, H, row_plan(G, n_q), d, n_seqs, &total);
+  ws_layout(nullptr, H, row_plan(G, n_q, dtype), d, n_seqs, &total);
   return total;
 }
 
 cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s) {
   AttendParams p{};
   p.a = a;
-  p.rp = row_plan(a.G, a.n_q);
+  p.rp = row_plan(a.G, a.n_q, a.dtype);
+  p.n_warps = (num_sms < kMaxCtas ? num_sms : kMaxCtas) * kWarps;
   p.ws = ws_layout(a.ws, a.H, p.rp, a.d, a.pg.n_seqs, nullptr);
   if (a.dtype == LOWRAM_DTYPE_BF16)
-    return a.d == 128 ? attend_d<__nv_bfloat16, 128, false>(p, num_sms, s)
-                      : attend_d<__nv_bfloat16, 64, false>(p, num_sms, s);
-  return a.d == 128 ? attend_d<float, 128, true>(p, num_sms, s)
-                    : attend_d<float, 64, true>(p, num_sms, s);
+    return a.d == 128 ? attend_d<__nv_bfloat16, 128, false>(p, s)
+                      : attend_d<__nv_bfloat16, 64, false>(p, s);
+  return a.d == 128 ? attend_d<float, 128, true>(p, s)
+                    : attend_d<float, 64, true>(p, s);
 }
 
 }  // namespace lowram
