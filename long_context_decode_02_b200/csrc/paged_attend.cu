@@ -108,17 +108,16 @@ struct AttendParams {
   int n_warps;   // of the attend kernel
 };
 
-// Steps of a warp's run, of `total` in the list.
-__device__ __forceinline__ long long run_steps(long long total, int n_warps) {
-  return total > 0 ? (total + n_warps - 1) / n_warps : 1;
+// x / y for y > 0, x >= 0: by 32 bits where they do (a 64-bit division is a tenth of a
+// microsecond, which the shortest calls see).
+__device__ __forceinline__ long long div_pos(long long x, int y) {
+  return x <= 0x7fffffffLL ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+// Steps of a warp's run, of `total` in the list: below 2^31 (n_seqs, pairs and lengths bound it).
+__device__ __forceinline__ int run_steps(long long total, int n_warps) {
+  return total > 0 ? (int)div_pos(total + n_warps - 1, n_warps) : 1;
 }
 
-__device__ __forceinline__ void grid_launch_dependents() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void grid_dependency_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -204,7 +203,9 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
     fence_mbar_init();
   }
   __syncthreads();
-  grid_launch_dependents();   // the merge may be set up; it waits for this grid's end
+  grid_dependency_wait();
+  // only now: the merge reads the lengths before its own wait, so what wrote them must have ended
+  grid_launch_dependents();
   volatile int* abort_flag = &s_abort;
 
   // ---- the list of steps
@@ -254,8 +255,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
   int uy = -1, off = 0;              // its unit of this lane: row of its box; the step's first unit
   int lst = 0, issued = 0;
   {   // where the run begins: sequence, pair, step
-    const long long steps = run_steps(total, p.n_warps);
-    const long long r0 = min(total, run * steps);
+    const int steps = run_steps(total, p.n_warps);
+    const long long r0 = min(total, (long long)run * steps);
     left = (int)(min(total, r0 + steps) - r0);
     long long at = 0;
     for (int b0 = 0; left > 0 && b0 < pg.n_seqs; b0 += 32) {
@@ -267,8 +268,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         llen = __shfl_sync(0xffffffffu, n, src);
         lns = steps_of(llen);
         const long long in = r0 - (at + __shfl_sync(0xffffffffu, x, src) - lns) * pairs;
-        lpair = (int)(in / lns);
-        lstep = (int)(in % lns);
+        lpair = (int)div_pos(in, lns);
+        lstep = (int)(in - (long long)lpair * lns);
         break;
       }
       at += __shfl_sync(0xffffffffu, x, 31);
@@ -319,19 +320,14 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
     }
   };
   auto issue = [&]() {
-    if (ccnt == 0) {                 // the next batch becomes the current one
+    const bool first = ccnt == 0;
+    if (first) {                     // the next batch becomes the current one
       if (!nscaled) look_up_scales();
       cb = nb; cpair = npair; ctok = ntok; clen = nlen; ccnt = ncnt; cslot = nslot; cflag = nflag;
       const int h = cpair / p.rp.groups;
       const int u = ctok / kUnit + lane;
       uy = nvalid > 0 ? (npage * a.H + h) * P + (u & ((1 << lgu) - 1)) * kUnit : -1;
       off = 0;
-      int ev = (int)((__float_as_uint(nsv) >> 23) & 255u) - 127;
-      ev = min(max(ev, -64), 120);
-      s_meta[warp][(U * issued + lane) & (kMetaUnits - 1)] =
-          make_float4(nsk, nsv * __int_as_float((127 - ev) << 23) * kWeightScale,
-                      __int_as_float(ev), __int_as_float(nvalid));
-      look_up();
     } else if (!nscaled) {
       look_up_scales();
     }
@@ -346,6 +342,14 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         tma_load_2d(dst, &maps.k, 0, uy, bar);
         tma_load_2d(dst + kHalfBytes, &maps.v, 0, uy, bar);
       }
+    }
+    if (first) {                     // behind the copies: the scales may still be on their way
+      int ev = (int)((__float_as_uint(nsv) >> 23) & 255u) - 127;
+      ev = min(max(ev, -64), 120);
+      s_meta[warp][(U * issued + lane) & (kMetaUnits - 1)] =
+          make_float4(nsk, nsv * __int_as_float((127 - ev) << 23) * kWeightScale,
+                      __int_as_float(ev), __int_as_float(nvalid));
+      look_up();
     }
     --ccnt;
     if (lane == 0) {
@@ -671,6 +675,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
   const int grp = r / p.rp.rows, rg = r % p.rp.rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = a.H * p.rp.groups, pair = h * p.rp.groups + grp;
+  grid_launch_dependents();
   long long total, before;
   int ns;
   if (pg.n_seqs <= 32) {
@@ -684,10 +689,10 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
     before = p.ws.first[b];
     ns = (int)(p.ws.first[b + 1] - before);
   }
-  const long long share = run_steps(total * pairs, p.n_warps);
+  const int share = run_steps(total * pairs, p.n_warps);
   const long long s0 = before * pairs + (long long)pair * ns;
-  const int first = (int)(s0 / share);
-  const int count = ns > 0 ? (int)((s0 + ns - 1) / share) - first + 1 : 0;
+  const int first = (int)div_pos(s0, share);
+  const int count = ns > 0 ? (int)div_pos(s0 + ns - 1, share) - first + 1 : 0;
   const size_t slot0 = (size_t)first + (size_t)b * pairs + pair;
   const float2* ml = p.ws.ml + slot0 * p.rp.rows + rg;
   const float* po = p.ws.o + (slot0 * p.rp.rows + rg) * D + lane * E;
@@ -756,19 +761,10 @@ cudaError_t attend_t(const AttendParams& p, cudaStream_t s) {
   auto kern = paged_attend_kernel<T, D, RL, F32>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<p.n_warps / kWarps, kWarps * 32, smem, s>>>(p, maps);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // set up while the first kernel runs
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(a.n_q * a.Hq, a.pg.n_seqs);
-  lc.blockDim = dim3(kCombineThreads);
-  lc.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  lc.attrs = &at;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelEx(&lc, paged_combine_kernel<T, D>, p);
+  e = launch_dependent(kern, dim3(p.n_warps / kWarps), kWarps * 32, smem, s, p, maps);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(paged_combine_kernel<T, D>, dim3(a.n_q * a.Hq, a.pg.n_seqs),
+                          kCombineThreads, 0, s, p);
 }
 
 template <typename T, int D, bool F32>

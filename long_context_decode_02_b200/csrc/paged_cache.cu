@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
   const int P = pg.page_tokens, b = blockIdx.y;
   const bool keys = (blockIdx.z & 1) == 0;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_launch_dependents();
+  grid_dependency_wait();
   int r0, n;
   if (a.cu_new) {
     r0 = a.cu_new[b];
@@ -207,6 +209,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs 
   const int P = pg.page_tokens, b = blockIdx.y;
   const uint8_t* codes = (const uint8_t*)(blockIdx.z ? pg.v_code : pg.k_code);
   const float* scales = blockIdx.z ? pg.v_scale : pg.k_scale;
+  grid_launch_dependents();
+  grid_dependency_wait();
   T* out = (T*)(blockIdx.z ? a.v_out : a.k_out) + (size_t)b * a.n * a.H * D;
   const int len = paged_len(pg, b, a.status);
   const int start = a.start ? a.start[b] : 0;
@@ -253,16 +257,17 @@ cudaError_t append_t(const PagedArgs& a, int num_sms, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<T, D>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  paged_append_kernel<T, D><<<dim3((unsigned)n_slots, a.pg.n_seqs, 2 * groups), kThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(paged_append_kernel<T, D>,
+                          dim3((unsigned)n_slots, a.pg.n_seqs, 2 * groups), kThreads, smem, s, a);
 }
 
 template <typename T, int D>
 cudaError_t gather_t(const PagedArgs& a, int num_sms, cudaStream_t s) {
   const int64_t blocks = ((int64_t)a.n * a.H * (D / 16) + kThreads - 1) / kThreads;
   const int64_t most = 64ll * num_sms;
-  paged_gather_kernel<T, D><<<dim3((unsigned)(blocks < most ? blocks : most), a.pg.n_seqs, 2), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(paged_gather_kernel<T, D>,
+                          dim3((unsigned)(blocks < most ? blocks : most), a.pg.n_seqs, 2),
+                          kThreads, 0, s, a);
 }
 
 }  // namespace

@@ -28,6 +28,33 @@ __device__ __forceinline__ uint32_t float4_to_e4m3x4(const float* x) {
   return float2_to_e4m3x2(x[0], x[1]) | (float2_to_e4m3x2(x[2], x[3]) << 16);
 }
 
+// The paged kernels are launched as programmatic dependents of whatever precedes them in the
+// stream: a kernel's blocks may be set up while the one before still runs, and touch memory only
+// behind grid_dependency_wait(), which returns when the kernels before have ended and their writes
+// are visible. (Back to back calls of an append and an attend: about 2 us less than plain
+// launches.)
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                             cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, P(args)...);
+}
+
 // Length of sequence b, cut to what its page list can hold (reported when it was not in range).
 __device__ __forceinline__ int paged_len(const lowram_pages& pg, int b, int* status) {
   const int n = pg.lens[b], top = pg.max_pages * pg.page_tokens;

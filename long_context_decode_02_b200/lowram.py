@@ -447,25 +447,32 @@ def paged_cache(k_code, v_code, k_scale, v_scale, table, lens) -> lowram_pages:
     p._refs = (k_code, v_code, k_scale, v_scale, table, lens)
     p._ref = ctypes.byref(p)
     p._heads = (k_code.shape[1], k_code.shape[3])
+    p._device = k_code.get_device()
     return p
 
 
 def _paged_check(ctx: Context, pages: lowram_pages, *tensors) -> None:
-    """The pages fit the context, and every tensor lies on its device."""
-    cfg = ctx.cfg
-    if pages._heads != (cfg.n_kv_heads, cfg.head_dim):
+    """The pages fit the context, and every tensor lies on its device, dense."""
+    if pages._heads != (ctx.cfg.n_kv_heads, ctx.cfg.head_dim):
         raise ValueError(f"pages of (heads, d) {pages._heads} in a context of "
-                         f"{(cfg.n_kv_heads, cfg.head_dim)}")
-    for t in (pages._refs[0],) + tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != ctx.device):
-            raise ValueError(f"tensor on {t.device}, context on cuda:{ctx.device}")
+                         f"{(ctx.cfg.n_kv_heads, ctx.cfg.head_dim)}")
+    dev = ctx.device
+    if pages._device != dev:
+        raise ValueError(f"pages on device {pages._device}, context on cuda:{dev}")
+    for t in tensors:
+        if t is not None:
+            if t.get_device() != dev:
+                raise ValueError(f"tensor on {t.device}, context on cuda:{dev}")
+            if not t.is_contiguous():
+                raise ValueError(f"tensor of shape {tuple(t.shape)} is not contiguous")
 
 
 def _paged_stream(ctx: Context, stream):
     """The given stream, or the current one of the context's device."""
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream(ctx.device)
-    return s.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(ctx.device)
 
 
 def _float_dtype(ctx: Context):
@@ -475,12 +482,12 @@ def _float_dtype(ctx: Context):
 
 def _int32(t, n: int, name: str):
     """Device address of an optional [n] int32 array."""
-    import torch
     if t is None:
         return None
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be int32 of shape ({n},), got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    return t.data_ptr()
 
 
 def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, max_new=None,
@@ -490,31 +497,39 @@ def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, m
     k_new / v_new may lie any multiple of 16 bytes apart (slices of a fused projection).
     pages' lens count the new tokens. cu_new [n_seqs + 1] int32 for ragged counts (max_new:
     the largest, default n_new)."""
-    cfg = ctx.cfg
-    _paged_check(ctx, pages, k_new, v_new, cu_new, pos_base)
-    H, d = cfg.n_kv_heads, cfg.head_dim
-    dt = _float_dtype(ctx)
-    if k_new.shape != v_new.shape or k_new.dim() not in (3, 4) or k_new.shape[-2:] != (H, d):
+    H, d = pages._heads
+    _paged_check(ctx, pages, cu_new, pos_base)
+    if k_new.get_device() != ctx.device or v_new.get_device() != ctx.device:
+        raise ValueError(f"k_new on {k_new.device}, v_new on {v_new.device}, context on "
+                         f"cuda:{ctx.device}")
+    shape = k_new.shape
+    if shape != v_new.shape or len(shape) not in (3, 4) or shape[-2] != H or shape[-1] != d:
         raise ValueError(f"k_new and v_new must be [n_new][{H}][{d}]")
-    if k_new.dim() == 4:
-        if k_new.shape[0] != pages.n_seqs:
-            raise ValueError(f"k_new holds {k_new.shape[0]} sequences, the pages {pages.n_seqs}")
-        _ptr(k_new), _ptr(v_new)    # contiguity check
-        k_new, v_new = k_new.flatten(0, 1), v_new.flatten(0, 1)
-    n = k_new.shape[0]
-    strides = []
-    for t in (k_new, v_new):
-        st = t.stride()
-        if t.dtype != dt:
-            raise ValueError(f"k_new and v_new must be {dt}")
-        if n and (st[2] != 1 or (st[1] != d and H > 1)):
-            raise ValueError("the heads of a token must be dense")
-        strides.append(st[0] if n > 1 else H * d)
-    cu = _int32(cu_new, pages.n_seqs + 1, "cu_new")
-    check(lowram_paged_append(ctx.handle, pages._ref, k_new.data_ptr(), v_new.data_ptr(),
-                              strides[0], strides[1], n, cu, n if max_new is None else max_new,
-                              _int32(pos_base, pages.n_seqs, "pos_base"), 1 if rotate else 0,
-                              _paged_stream(ctx, stream)), "lowram_paged_append")
+    dt = _float_dtype(ctx)
+    if k_new.dtype != dt or v_new.dtype != dt:
+        raise ValueError(f"k_new and v_new must be {dt}")
+    if len(shape) == 4:
+        if shape[0] != pages.n_seqs:
+            raise ValueError(f"k_new holds {shape[0]} sequences, the pages {pages.n_seqs}")
+        if not (k_new.is_contiguous() and v_new.is_contiguous()):
+            raise ValueError("4-dimensional k_new and v_new must be contiguous")
+        n, ks, vs = shape[0] * shape[1], H * d, H * d
+    else:
+        n, ks, vs = shape[0], H * d, H * d
+        if n:
+            a, b = k_new.stride(), v_new.stride()
+            if a[2] != 1 or b[2] != 1 or (H > 1 and (a[1] != d or b[1] != d)):
+                raise ValueError("the heads of a token must be dense")
+            if n > 1:
+                ks, vs = a[0], b[0]
+    n_seqs = pages.n_seqs
+    st = lowram_paged_append(ctx._h, pages._ref, k_new.data_ptr(), v_new.data_ptr(), ks, vs, n,
+                             _int32(cu_new, n_seqs + 1, "cu_new"),
+                             n if max_new is None else max_new,
+                             _int32(pos_base, n_seqs, "pos_base"), 1 if rotate else 0,
+                             _paged_stream(ctx, stream))
+    if st != OK:
+        raise LowRAMError(st, "lowram_paged_append")
 
 
 def paged_workspace_size(cfg: lowram_config, n_seqs: int, n_q: int = 1) -> int:
@@ -529,37 +544,38 @@ def paged_attend(ctx: Context, pages: lowram_pages, q, out, workspace, lse=None,
     """lowram_paged_attend: attention of q [n_seqs][n_q][H_q][d] (or [n_seqs][H_q][d]: one
     query a sequence) over the pages; out like q, lse [n_seqs][n_q][H_q] fp32."""
     import torch
-    cfg = ctx.cfg
     _paged_check(ctx, pages, q, out, workspace, lse)
     dt = _float_dtype(ctx)
     shape = q.shape
-    if (len(shape) not in (3, 4) or shape[0] != pages.n_seqs or shape[-2] != cfg.n_q_heads or
-            shape[-1] != cfg.head_dim or out.shape != shape):
-        raise ValueError(f"q and out must be [{pages.n_seqs}][n_q][{cfg.n_q_heads}]"
-                         f"[{cfg.head_dim}]")
+    if (len(shape) not in (3, 4) or shape[0] != pages.n_seqs or shape[-2] != ctx.cfg.n_q_heads or
+            shape[-1] != pages._heads[1] or out.shape != shape):
+        raise ValueError(f"q and out must be [{pages.n_seqs}][n_q][{ctx.cfg.n_q_heads}]"
+                         f"[{pages._heads[1]}]")
     if q.dtype != dt or out.dtype != dt:
         raise ValueError(f"q and out must be {dt}")
-    n_q = shape[1] if len(shape) == 4 else 1
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1]):
         raise ValueError(f"lse must be fp32 of shape {tuple(shape[:-1])}")
-    check(lowram_paged_attend(ctx.handle, pages._ref, _ptr(q), n_q, _ptr(out), _ptr(lse),
-                              _ptr(workspace), workspace.numel() * workspace.element_size(),
-                              _paged_stream(ctx, stream)), "lowram_paged_attend")
+    st = lowram_paged_attend(ctx._h, pages._ref, q.data_ptr(), shape[1] if len(shape) == 4 else 1,
+                             out.data_ptr(), None if lse is None else lse.data_ptr(),
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                             _paged_stream(ctx, stream))
+    if st != OK:
+        raise LowRAMError(st, "lowram_paged_attend")
 
 
 def paged_gather(ctx: Context, pages: lowram_pages, k_out, v_out, start=None,
                  stream=None) -> None:
     """lowram_paged_gather: tokens start[b] .. of every sequence (default 0) read out of the
     pages into k_out, v_out [n_seqs][n][H][d]; zeros outside the sequence."""
-    cfg = ctx.cfg
     _paged_check(ctx, pages, k_out, v_out, start)
     shape = k_out.shape
     if (len(shape) != 4 or shape[0] != pages.n_seqs or
-            tuple(shape[2:]) != (cfg.n_kv_heads, cfg.head_dim) or v_out.shape != shape):
-        raise ValueError(f"k_out and v_out must be [{pages.n_seqs}][n][{cfg.n_kv_heads}]"
-                         f"[{cfg.head_dim}]")
-    if k_out.dtype != _float_dtype(ctx) or v_out.dtype != _float_dtype(ctx):
-        raise ValueError(f"k_out and v_out must be {_float_dtype(ctx)}")
-    check(lowram_paged_gather(ctx.handle, pages._ref, _int32(start, pages.n_seqs, "start"),
-                              shape[1], _ptr(k_out), _ptr(v_out), _paged_stream(ctx, stream)),
-          "lowram_paged_gather")
+            (shape[2], shape[3]) != pages._heads or v_out.shape != shape):
+        raise ValueError(f"k_out and v_out must be [{pages.n_seqs}][n][H, d = {pages._heads}]")
+    dt = _float_dtype(ctx)
+    if k_out.dtype != dt or v_out.dtype != dt:
+        raise ValueError(f"k_out and v_out must be {dt}")
+    st = lowram_paged_gather(ctx._h, pages._ref, _int32(start, pages.n_seqs, "start"), shape[1],
+                             k_out.data_ptr(), v_out.data_ptr(), _paged_stream(ctx, stream))
+    if st != OK:
+        raise LowRAMError(st, "lowram_paged_gather")
