@@ -947,7 +947,7 @@ lowram_status lowram_paged_gather(lowram_ctx* ctx, const lowram_pages* pages,
   a.n = n;
   a.k_out = k_out;
   a.v_out = v_out;
-  if (launch_paged_gather(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  if (launch_paged_gather(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return LOWRAM_ERR_CUDA;
   }

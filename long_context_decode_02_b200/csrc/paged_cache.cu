@@ -102,9 +102,19 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
   const int lo = max(first, p0) - p0, hi = min(len, p0 + P) - p0;   // new rows lo .. hi-1
   const bool rotate = keys && a.rotate;
   if (rotate) {
-    for (int o = tid; o < (hi - lo) * kHalf; o += kThreads) {
-      const int r = lo + o / kHalf, i = o % kHalf;
-      s_trig[r * kHalf + i] = rope_any64(a.rope, i, base + p0 + r);
+    // a thread takes one pair and consecutive rows: the first from the tables, the others by
+    // turning on by theta_i (at most 16 turns: 2^-49)
+    constexpr int kPer = kThreads / kHalf;                 // threads of a pair
+    const int i = tid % kHalf, rows = (hi - lo + kPer - 1) / kPer;
+    const int ra = lo + (tid / kHalf) * rows, rb = min(hi, ra + rows);
+    if (ra < rb) {
+      const double2 d = a.rope.lo64[a.rope.half + i];      // (cos, sin)(theta_i)
+      double2 c = rope_any64(a.rope, i, base + p0 + ra);
+      s_trig[ra * kHalf + i] = c;
+      for (int r = ra + 1; r < rb; ++r) {
+        c = make_double2(c.x * d.x - c.y * d.y, c.y * d.x + c.x * d.y);
+        s_trig[r * kHalf + i] = c;
+      }
     }
     __syncthreads();
   }
@@ -201,47 +211,69 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
   }
 }
 
-// Gather: 16 codes a thread, k_out then v_out. Bound by bytes: 2 B n H d (1 + es).
+// Gather. Bound by bytes: 2 B n H d (1 + es). A warp takes the rows of one page and head, keys or
+// values: one look-up of page and scale, then 16-byte stores, a row's 128 or 256 bytes at a time,
+// with the codes of eight stores in flight.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs a) {
-  constexpr int kVec = D / 16;
+  constexpr int E = 16 / sizeof(T), kLanes = D / E;   // codes of a store, lanes of a row
+  constexpr int kRows = 32 / kLanes > 0 ? 32 / kLanes : 1, kParts = kLanes > 32 ? kLanes / 32 : 1;
   const lowram_pages& pg = a.pg;
   const int P = pg.page_tokens, b = blockIdx.y;
-  const uint8_t* codes = (const uint8_t*)(blockIdx.z ? pg.v_code : pg.k_code);
-  const float* scales = blockIdx.z ? pg.v_scale : pg.k_scale;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_launch_dependents();
   grid_dependency_wait();
+  const uint8_t* codes = (const uint8_t*)(blockIdx.z ? pg.v_code : pg.k_code);
+  const float* scales = blockIdx.z ? pg.v_scale : pg.k_scale;
   T* out = (T*)(blockIdx.z ? a.v_out : a.k_out) + (size_t)b * a.n * a.H * D;
   const int len = paged_len(pg, b, a.status);
-  const int start = a.start ? a.start[b] : 0;
-  const int64_t total = (int64_t)a.n * a.H * kVec;
-  for (int64_t o = (int64_t)blockIdx.x * kThreads + threadIdx.x; o < total;
-       o += (int64_t)gridDim.x * kThreads) {
-    const int v = (int)(o % kVec), h = (int)(o / kVec % a.H), i = (int)(o / kVec / a.H);
-    const int64_t t = (int64_t)start + i;
-    float x[16];
+  const int64_t start = a.start ? a.start[b] : 0;
+  const int64_t p0 = start >= 0 ? start / P : -((P - 1 - start) / P);   // floor
+  const int64_t unit = (int64_t)blockIdx.x * (kThreads / 32) + warp;
+  const int64_t pi = p0 + unit / a.H;
+  const int h = (int)(unit % a.H);
+  // rows of the page inside the run
+  const int64_t t0 = pi * P;
+  const int lo = (int)max((int64_t)0, start - t0), hi = (int)min((int64_t)P, start + a.n - t0);
+  if (lo >= hi) return;
+  int page = -1;
+  if (t0 + hi > 0 && t0 + lo < len && t0 >= 0) page = paged_page(pg, b, (int)pi, a.status);
+  const int held = page < 0 ? 0 : (int)min((int64_t)hi, len - t0);   // rows lo .. held-1 are tokens
+  const size_t ph = (size_t)(page < 0 ? 0 : page) * a.H + h;
+  const float s = page < 0 ? 0.f : scales[ph];
+  const uint8_t* src = codes + ph * (size_t)P * D;
+  const int r0 = lane / kLanes, el = (lane % kLanes) * E;
+  constexpr int kU = 8;
+  for (int r = lo; r < hi; r += kU * kRows / kParts) {
+    uint32_t w[kU][E / 4];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = 0.f;
-    if (t >= 0 && t < len) {
-      const int page = paged_page(pg, b, (int)t / P, a.status);
-      if (page >= 0) {
-        const size_t ph = (size_t)page * a.H + h;
-        const float s = scales[ph];
-        const uint4 w = *reinterpret_cast<const uint4*>(codes + (ph * P + (int)t % P) * D + 16 * v);
-        e4m3x4_to_float(w.x, x);
-        e4m3x4_to_float(w.y, x + 4);
-        e4m3x4_to_float(w.z, x + 8);
-        e4m3x4_to_float(w.w, x + 12);
+    for (int k = 0; k < kU; ++k) {
+      const int row = r + (k / kParts) * kRows + r0, e0 = el + (k % kParts) * 32 * E;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] *= s;
+      for (int e = 0; e < E / 4; ++e) w[k][e] = 0;
+      if (row < held) {
+        if constexpr (E == 8) {
+          const uint2 y = *reinterpret_cast<const uint2*>(src + row * D + e0);
+          w[k][0] = y.x;
+          w[k][1] = y.y;
+        } else {
+          w[k][0] = *reinterpret_cast<const uint32_t*>(src + row * D + e0);
+        }
       }
     }
-    T y[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = from_f<T>(x[e]);
-    uint4* dst = reinterpret_cast<uint4*>(out + ((size_t)i * a.H + h) * D + 16 * v);
+    for (int k = 0; k < kU; ++k) {
+      const int row = r + (k / kParts) * kRows + r0, e0 = el + (k % kParts) * 32 * E;
+      if (row >= hi) continue;
+      float x[E];
+      alignas(16) T y[E];
 #pragma unroll
-    for (int e = 0; e < (int)sizeof(y) / 16; ++e) dst[e] = reinterpret_cast<const uint4*>(y)[e];
+      for (int e = 0; e < E / 4; ++e) e4m3x4_to_float(w[k][e], x + 4 * e);
+#pragma unroll
+      for (int e = 0; e < E; ++e) y[e] = from_f<T>(x[e] * s);
+      *reinterpret_cast<uint4*>(out + ((size_t)(t0 + row - start) * a.H + h) * D + e0) =
+          *reinterpret_cast<const uint4*>(y);
+    }
   }
 }
 
@@ -262,11 +294,12 @@ cudaError_t append_t(const PagedArgs& a, int num_sms, cudaStream_t s) {
 }
 
 template <typename T, int D>
-cudaError_t gather_t(const PagedArgs& a, int num_sms, cudaStream_t s) {
-  const int64_t blocks = ((int64_t)a.n * a.H * (D / 16) + kThreads - 1) / kThreads;
-  const int64_t most = 64ll * num_sms;
+cudaError_t gather_t(const PagedArgs& a, cudaStream_t s) {
+  const int P = a.pg.page_tokens;
+  const int64_t units = ((int64_t)(a.n - 1) / P + 2) * a.H;   // pages a run can touch
   return launch_dependent(paged_gather_kernel<T, D>,
-                          dim3((unsigned)(blocks < most ? blocks : most), a.pg.n_seqs, 2),
+                          dim3((unsigned)((units + kThreads / 32 - 1) / (kThreads / 32)),
+                               a.pg.n_seqs, 2),
                           kThreads, 0, s, a);
 }
 
@@ -279,11 +312,11 @@ cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s)
   return a.d == 128 ? append_t<float, 128>(a, num_sms, s) : append_t<float, 64>(a, num_sms, s);
 }
 
-cudaError_t launch_paged_gather(const PagedArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_paged_gather(const PagedArgs& a, cudaStream_t s) {
   if (a.dtype == LOWRAM_DTYPE_BF16)
-    return a.d == 128 ? gather_t<__nv_bfloat16, 128>(a, num_sms, s)
-                      : gather_t<__nv_bfloat16, 64>(a, num_sms, s);
-  return a.d == 128 ? gather_t<float, 128>(a, num_sms, s) : gather_t<float, 64>(a, num_sms, s);
+    return a.d == 128 ? gather_t<__nv_bfloat16, 128>(a, s)
+                      : gather_t<__nv_bfloat16, 64>(a, s);
+  return a.d == 128 ? gather_t<float, 128>(a, s) : gather_t<float, 64>(a, s);
 }
 
 }  // namespace lowram
