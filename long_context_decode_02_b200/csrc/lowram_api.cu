@@ -884,7 +884,7 @@ lowram_status lowram_paged_append(lowram_ctx* ctx, const lowram_pages* pages, co
   a.max_new = cu_new ? max_new : n_new / pages->n_seqs;
   a.pos_base = pos_base;
   a.rotate = rotate;
-  if (launch_paged_append(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+  if (launch_paged_append(a, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return LOWRAM_ERR_CUDA;
   }

@@ -232,7 +232,7 @@ struct PagedArgs {
   // gather
   const int32_t* start; int n; void* k_out; void* v_out;
 };
-cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedArgs& a, cudaStream_t s);
 cudaError_t launch_paged_gather(const PagedArgs& a, cudaStream_t s);
 size_t paged_attend_workspace_bytes(int H, int G, int d, int dtype, int n_seqs, int n_q);
 cudaError_t launch_paged_attend(const PagedArgs& a, int num_sms, cudaStream_t s);

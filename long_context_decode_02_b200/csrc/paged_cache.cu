@@ -8,18 +8,24 @@
 // the code becomes subnormal, so it does not matter (to 2^-10 s) in how many calls a page was
 // filled; a scale amax / 448 would gain nothing, since e4m3's steps are relative.
 //
-// Bound by bytes: 2 N H d (es + 1). One CTA takes one (page, keys or values) of a sequence and
-// all heads or a share of them: a warp holds 16 rows of one head in registers, so the input is
-// read once, and the (cos, sin) of the page's positions are formed once in fp64 (three table
-// levels, two angle additions) into shared memory for all heads. Angles and products are fp64
-// (four operations a pair) because e4m3's rounding and the scale's power of two are decisions:
-// an fp32 rotation would flip one in about 2^20 of them against the formula.
+// Bound by bytes: 2 N H d (es + 1). A warp takes 16 rows of one page and head, keys or values; the
+// 1, 2 or 4 warps of a (page, head) agree on its maximum. A lane holds the same two pairs (four
+// elements) of each of its rows in registers, so the input is read once, and turns its (cos, sin)
+// on from row to row by theta_i: one look-up (three table levels) a warp, four fp64 operations a
+// row and pair, no shared memory. Angles and products are fp64 because e4m3's rounding and the
+// scale's power of two are decisions: an fp32 rotation would flip one in about 2^20 of them
+// against the formula. Short-lived CTAs, five an SM, keep the loads in flight; a CTA that went
+// over several (page, head)s and requested the next rows early took twice as long (112 us against
+// 50 for 23.3K tokens of 8 heads, pages of 64): 128 registers a thread were not enough for both.
+#include <type_traits>
+
 #include "paged_common.cuh"
 
 namespace lowram {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // gather
+constexpr int kAppendThreads = 128;
 constexpr int kRowsPerWarp = 16;
 
 // (cos, sin)(pos * theta_i), pos < 2^24
@@ -39,43 +45,37 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 }
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
-template <typename T, int E> struct RowLoad;   // E consecutive elements as floats
-template <> struct RowLoad<__nv_bfloat16, 4> {
-  __device__ static void load(const __nv_bfloat16* p, float* o) { VecLoad<__nv_bfloat16, 4>::load(p, o); }
+// Two consecutive elements as loaded, and as floats.
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+  using Raw = uint32_t;
+  static __device__ __forceinline__ float2 get(Raw r) { return bf2_to_f2(r); }
 };
-template <> struct RowLoad<__nv_bfloat16, 2> {
-  __device__ static void load(const __nv_bfloat16* p, float* o) { VecLoad<__nv_bfloat16, 2>::load(p, o); }
-};
-template <> struct RowLoad<float, 4> {
-  __device__ static void load(const float* p, float* o) { VecLoad<float, 4>::load(p, o); }
-};
-template <> struct RowLoad<float, 2> {
-  __device__ static void load(const float* p, float* o) { VecLoad<float, 2>::load(p, o); }
+template <> struct Two<float> {
+  using Raw = float2;
+  static __device__ __forceinline__ float2 get(Raw r) { return r; }
 };
 
-template <int E> __device__ __forceinline__ void store_codes(uint8_t* p, const float* x);
-template <> __device__ __forceinline__ void store_codes<4>(uint8_t* p, const float* x) {
-  *reinterpret_cast<uint32_t*>(p) = float4_to_e4m3x4(x);
-}
-template <> __device__ __forceinline__ void store_codes<2>(uint8_t* p, const float* x) {
-  *reinterpret_cast<uint16_t*>(p) = (uint16_t)float2_to_e4m3x2(x[0], x[1]);
+__device__ __forceinline__ double2 turn(double2 c, double2 d) {   // angles added
+  return make_double2(c.x * d.x - c.y * d.y, c.y * d.x + c.x * d.y);
 }
 
-// grid (pages of a sequence, n_seqs, 2 * head groups); dynamic shared memory: page_tokens * d/2
-// double2 (rotation). Lane l of a warp: rows 2 k + (l >> 4), elements E (l & 15) .. of the row's
-// first and second half.
+// grid (units of a sequence / teams, n_seqs, 2): a unit is a (page, head), a team the warps of one.
+// Lane l: pairs 2 (l % LR), + 1 of rows l / LR + RS k.
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs a) {
-  constexpr int kHalf = D / 2, E = kHalf / 16, kRows = kRowsPerWarp / 2;
-  extern __shared__ double2 s_trig[];
-  __shared__ float s_amax[kThreads / 32];
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 5 : 4)
+paged_append_kernel(const PagedArgs a) {
+  using Raw = typename Two<T>::Raw;
+  constexpr int kHalf = D / 2, LR = kHalf / 2, RS = 32 / LR, NR = kRowsPerWarp / RS;
+  __shared__ float s_amax[kAppendThreads / 32];
   const lowram_pages& pg = a.pg;
   const int P = pg.page_tokens, b = blockIdx.y;
-  const bool keys = (blockIdx.z & 1) == 0;
+  const bool keys = blockIdx.z == 0, rotate = keys && a.rotate;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   int r0, n;
+  const int len = pg.lens[b], base = a.pos_base ? a.pos_base[b] : 0;
   if (a.cu_new) {
     r0 = a.cu_new[b];
     n = a.cu_new[b + 1] - r0;
@@ -88,125 +88,145 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedArgs 
     r0 = b * n;
   }
   if (n == 0) return;
-  const int len = pg.lens[b], first = len - n;
-  const int base = a.pos_base ? a.pos_base[b] : 0;
+  const int first = len - n;
   if (first < 0 || len > pg.max_pages * P ||
       (a.rotate && (base < -first || base > kMaxPosition - len))) {
     if (blockIdx.x == 0 && tid == 0) raise_status(a.status, kStatusDeviceCheck);
     return;
   }
-  const int pi = first / P + blockIdx.x, p0 = pi * P;   // the page's first token
-  if (p0 >= len) return;
-  const int page = paged_page(pg, b, pi, a.status);
-  if (page < 0) return;
-  const int lo = max(first, p0) - p0, hi = min(len, p0 + P) - p0;   // new rows lo .. hi-1
-  const bool rotate = keys && a.rotate;
-  if (rotate) {
-    // a thread takes one pair and consecutive rows: the first from the tables, the others by
-    // turning on by theta_i (at most 16 turns: 2^-49)
-    constexpr int kPer = kThreads / kHalf;                 // threads of a pair
-    const int i = tid % kHalf, rows = (hi - lo + kPer - 1) / kPer;
-    const int ra = lo + (tid / kHalf) * rows, rb = min(hi, ra + rows);
-    if (ra < rb) {
-      const double2 d = a.rope.lo64[a.rope.half + i];      // (cos, sin)(theta_i)
-      double2 c = rope_any64(a.rope, i, base + p0 + ra);
-      s_trig[ra * kHalf + i] = c;
-      for (int r = ra + 1; r < rb; ++r) {
-        c = make_double2(c.x * d.x - c.y * d.y, c.y * d.x + c.x * d.y);
-        s_trig[r * kHalf + i] = c;
-      }
-    }
-    __syncthreads();
-  }
-  const T* src = (const T*)(keys ? a.k_new : a.v_new) ;
+  const T* src = (const T*)(keys ? a.k_new : a.v_new);
   const int64_t stride = keys ? a.k_stride : a.v_stride;
   uint8_t* codes = (uint8_t*)(keys ? pg.k_code : pg.v_code);
   float* scales = keys ? pg.k_scale : pg.v_scale;
-  const int wt = P / kRowsPerWarp;                     // warps of a head's team
-  const int teams = (kThreads / 32) / wt, team = warp / wt;
-  const int row0 = (warp % wt) * kRowsPerWarp + (lane >> 4);
-  const int el = E * (lane & 15);
-  const int groups = gridDim.z >> 1, hpg = (a.H + groups - 1) / groups;
-  const int h_begin = (blockIdx.z >> 1) * hpg, h_end = min(a.H, h_begin + hpg);
-  for (int h0 = h_begin; h0 < h_end; h0 += teams) {
-    const int h = h0 + team;
-    const bool mine = h < h_end;
-    float x[kRows][2 * E];
-    float amax = 0.f;
-    if (mine) {
+  const int wt = P / kRowsPerWarp, teams = (kAppendThreads / 32) / wt, team = warp / wt;
+  const int page0 = first / P;
+  const int units = ((len - 1) / P - page0 + 1) * a.H;
+  if ((int)blockIdx.x * teams >= units) return;   // the whole CTA
+  const int unit = blockIdx.x * teams + team;
+  const bool mine = unit < units;
+  const int row0 = (warp % wt) * kRowsPerWarp + lane / LR;   // this lane's first row
+  const int i0 = 2 * (lane % LR);                             // its pairs i0, i0 + 1
+  const int pi = page0 + unit / a.H, h = unit % a.H, p0 = pi * P;
+  const int lo = max(first, p0) - p0, hi = min(len, p0 + P) - p0;   // new rows lo .. hi-1
+  const int wrow = (warp % wt) * kRowsPerWarp;   // the warp's rows wrow .. wrow + 15
+  const bool any = mine && wrow < hi && wrow + kRowsPerWarp > lo;
+  const bool all = any && wrow >= lo && wrow + kRowsPerWarp <= hi;
+  float x[NR][4];   // pair i0's first and second element, pair i0 + 1's
+  float amax = 0.f;
+  // ROT: rotated keys. ALL: every row of the warp is new, as in all pages of a long prompt but
+  // its ends (a third of the instructions are the others' comparisons).
+  auto take = [&](auto rot, auto all_rows) {
+    constexpr bool ROT = decltype(rot)::value, ALL = decltype(all_rows)::value;
+    Raw raw[NR][2];
+    const T* p = src + (int64_t)(r0 + p0 + row0 - first) * stride + (int64_t)h * D + i0;
+    const int64_t step = RS * stride;
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int r = row0 + 2 * k;
-        if (r >= lo && r < hi) {
-          const T* p = src + (int64_t)(r0 + p0 + r - first) * stride + (int64_t)h * D + el;
-          RowLoad<T, E>::load(p, x[k]);
-          RowLoad<T, E>::load(p + kHalf, x[k] + E);
-        }
+    for (int k = 0; k < NR; ++k, p += step) {
+      const int r = row0 + RS * k;
+      if (ALL || (r >= lo && r < hi)) {
+        raw[k][0] = *reinterpret_cast<const Raw*>(p);
+        raw[k][1] = *reinterpret_cast<const Raw*>(p + kHalf);
       }
+    }
+    double2 c[2], d[2];
+    if (ROT) {
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int r = row0 + 2 * k;
-        if (r >= lo && r < hi) {
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            if (rotate) {
-              const double2 cs = s_trig[r * kHalf + el + e];
-              const double u = x[k][e], v = x[k][E + e];
-              x[k][e] = (float)(u * cs.x - v * cs.y);
-              x[k][E + e] = (float)(u * cs.y + v * cs.x);
-            }
-          }
-#pragma unroll
-          for (int e = 0; e < 2 * E; ++e) {
-            const float m = fabsf(x[k][e]);
-            if (m <= 3.402823466e38f) amax = fmaxf(amax, m);
-            else x[k][e] = __int_as_float(0x7fffffff);   // infinities become NaN codes
-          }
-        }
+      for (int e = 0; e < 2; ++e) {
+        // rows before the sequence's first may lie below position 0, rows behind its last above
+        // the tables
+        const int pos = min(base + p0 + row0, kMaxPosition - 1);
+        c[e] = rope_any64(a.rope, i0 + e, pos < 0 ? -pos : pos);
+        if (pos < 0) c[e].y = -c[e].y;
+        d[e] = a.rope.lo64[RS * a.rope.half + i0 + e];
       }
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const size_t ph = (size_t)page * a.H + (mine ? h : 0);
-    const float old = mine && lo > 0 ? scales[ph] : 0.f;
-    if (wt > 1) {   // the team's maximum; everyone has read the old scale before it is replaced
-      if (lane == 0) s_amax[warp] = amax;
-      __syncthreads();
-      amax = s_amax[team * wt];
-      for (int w = 1; w < wt; ++w) amax = fmaxf(amax, s_amax[team * wt + w]);
-      __syncthreads();
-    } else {
-      __syncwarp();
-    }
-    if (!mine) continue;
-    const float fresh = pow2f(scale_exponent(amax));
-    const float s = fmaxf(fresh, old);
-    if (warp % wt == 0 && lane == 0) scales[ph] = s;
-    uint8_t* dst = codes + ph * (size_t)P * D;
-    const float inv = 1.0f / s;   // exact: a power of two between 2^-120 and 2^64
+    for (int k = 0; k < NR; ++k) {
+      const int r = row0 + RS * k;
+      if (ALL || (r >= lo && r < hi)) {
+        const float2 u = Two<T>::get(raw[k][0]), v = Two<T>::get(raw[k][1]);
+        x[k][0] = u.x;
+        x[k][1] = v.x;
+        x[k][2] = u.y;
+        x[k][3] = v.y;
+        if (ROT) {
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int r = row0 + 2 * k;
+          for (int e = 0; e < 2; ++e) {
+            const double y = x[k][2 * e], z = x[k][2 * e + 1];
+            x[k][2 * e] = (float)(y * c[e].x - z * c[e].y);
+            x[k][2 * e + 1] = (float)(y * c[e].y + z * c[e].x);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fabsf(x[k][e]));   // skips NaN
+      }
+      if (ROT && k + 1 < NR) {
+        c[0] = turn(c[0], d[0]);
+        c[1] = turn(c[1], d[1]);
+      }
+    }
+  };
+  if (all) {
+    if (rotate) take(std::true_type(), std::true_type());
+    else take(std::false_type(), std::true_type());
+  } else if (any) {
+    if (rotate) take(std::true_type(), std::false_type());
+    else take(std::false_type(), std::false_type());
+  }
+  if (!(amax <= 3.402823466e38f)) {   // infinities become NaN codes and do not count
+    amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < NR; ++k) {
+      const int r = row0 + RS * k;
       if (r >= lo && r < hi) {
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) x[k][e] *= inv;
-        store_codes<E>(dst + r * D + el, x[k]);
-        store_codes<E>(dst + r * D + kHalf + el, x[k] + E);
+        for (int e = 0; e < 4; ++e) {
+          if (fabsf(x[k][e]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(x[k][e]));
+          else x[k][e] = __int_as_float(0x7fffffff);
+        }
       }
     }
-    if (lo > 0 && s > old) {   // earlier tokens of the page, at the larger scale
-      const float ratio = old * inv;
-      const int rw = (warp % wt) * kRowsPerWarp;
-      for (int o = lane; o < kRowsPerWarp * (D / 4); o += 32) {
-        const int r = rw + o / (D / 4);
-        if (r >= lo) break;
-        uint32_t* w = reinterpret_cast<uint32_t*>(dst + r * D) + o % (D / 4);
-        float f[4];
-        e4m3x4_to_float(*w, f);
+  }
+  const int page = mine ? paged_page(pg, b, pi, a.status) : -1;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] *= ratio;
-        *w = float4_to_e4m3x4(f);
-      }
+  for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const size_t ph = (size_t)(page < 0 ? 0 : page) * a.H + h;
+  const float old = page >= 0 && lo > 0 ? scales[ph] : 0.f;
+  if (wt > 1) {   // the team's maximum; everyone has read the old scale before it is replaced
+    if (lane == 0) s_amax[warp] = amax;
+    __syncthreads();
+    amax = s_amax[team * wt];
+    for (int w = 1; w < wt; ++w) amax = fmaxf(amax, s_amax[team * wt + w]);
+  } else {
+    __syncwarp();
+  }
+  if (page < 0) return;
+  const float s = fmaxf(pow2f(scale_exponent(amax)), old);
+  if (warp % wt == 0 && lane == 0) scales[ph] = s;
+  uint8_t* dst = codes + ph * (size_t)P * D;
+  const float inv = 1.0f / s;   // exact: a power of two between 2^-120 and 2^64
+  uint8_t* q = dst + row0 * D + i0;
+#pragma unroll
+  for (int k = 0; k < NR; ++k) {
+    const int r = row0 + RS * k;
+    if (all || (r >= lo && r < hi)) {
+      *reinterpret_cast<uint16_t*>(q + RS * k * D) =
+          (uint16_t)float2_to_e4m3x2(x[k][0] * inv, x[k][2] * inv);
+      *reinterpret_cast<uint16_t*>(q + RS * k * D + kHalf) =
+          (uint16_t)float2_to_e4m3x2(x[k][1] * inv, x[k][3] * inv);
+    }
+  }
+  if (lo > 0 && s > old) {   // earlier tokens of the page, at the larger scale
+    const float ratio = old * inv;
+    for (int o = lane; o < kRowsPerWarp * (D / 4); o += 32) {
+      const int r = wrow + o / (D / 4);
+      if (r >= lo) break;
+      uint32_t* w = reinterpret_cast<uint32_t*>(dst + r * D) + o % (D / 4);
+      float f[4];
+      e4m3x4_to_float(*w, f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] *= ratio;
+      *w = float4_to_e4m3x4(f);
     }
   }
 }
@@ -278,19 +298,13 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs 
 }
 
 template <typename T, int D>
-cudaError_t append_t(const PagedArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t append_t(const PagedArgs& a, cudaStream_t s) {
   const int P = a.pg.page_tokens;
-  const int64_t n_slots = ((int64_t)a.max_new + 2 * P - 2) / P;   // pages n tokens can touch
-  const int teams = (kThreads / 32) / (P / kRowsPerWarp);
-  const int passes = (a.H + teams - 1) / teams;
-  // few CTAs: a share of the heads each; many: all heads, so that a page's angles are formed once
-  const int groups = n_slots * a.pg.n_seqs * 2 * passes <= 4 * num_sms ? passes : 1;
-  const size_t smem = a.rotate ? (size_t)P * (D / 2) * sizeof(double2) : 0;
-  cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<T, D>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  const int64_t units = ((int64_t)a.max_new + 2 * P - 2) / P * a.H;   // (page, head)s of n tokens
+  const int teams = (kAppendThreads / 32) / (P / kRowsPerWarp);
   return launch_dependent(paged_append_kernel<T, D>,
-                          dim3((unsigned)n_slots, a.pg.n_seqs, 2 * groups), kThreads, smem, s, a);
+                          dim3((unsigned)((units + teams - 1) / teams), a.pg.n_seqs, 2), kAppendThreads,
+                          0, s, a);
 }
 
 template <typename T, int D>
@@ -305,11 +319,11 @@ cudaError_t gather_t(const PagedArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedArgs& a, int num_sms, cudaStream_t s) {
+cudaError_t launch_paged_append(const PagedArgs& a, cudaStream_t s) {
   if (a.dtype == LOWRAM_DTYPE_BF16)
-    return a.d == 128 ? append_t<__nv_bfloat16, 128>(a, num_sms, s)
-                      : append_t<__nv_bfloat16, 64>(a, num_sms, s);
-  return a.d == 128 ? append_t<float, 128>(a, num_sms, s) : append_t<float, 64>(a, num_sms, s);
+    return a.d == 128 ? append_t<__nv_bfloat16, 128>(a, s)
+                      : append_t<__nv_bfloat16, 64>(a, s);
+  return a.d == 128 ? append_t<float, 128>(a, s) : append_t<float, 64>(a, s);
 }
 
 cudaError_t launch_paged_gather(const PagedArgs& a, cudaStream_t s) {
