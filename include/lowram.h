@@ -363,6 +363,19 @@ lowram_status lowram_paged_attend(lowram_ctx* ctx, const lowram_pages* pages, co
 lowram_status lowram_paged_workspace_size(const lowram_config* cfg, int32_t n_seqs, int32_t n_q,
                                           size_t* bytes);
 
+/* One decode step over the compressed prefix plus a paged 8-bit suffix of generated tokens: as
+ * lowram_decode_step_suffix, with the suffix in `pages`, so every batch element has its own
+ * suffix length (0 allowed) and the generated tokens take half the memory. One softmax spans
+ * the selected chunks' rebuilt tokens and every token in the pages.
+ *   q, out, sel_out as in lowram_decode_step; pages->n_seqs == cfg->batch (LOWRAM_ERR_SHAPE
+ *   otherwise). Any configuration that lowram_decode_step takes.
+ * Workspace: lowram_decode_paged_workspace_size(cfg). */
+lowram_status lowram_decode_step_paged(lowram_ctx* ctx, const lowram_cache* cache,
+                                       const lowram_layer_params* params, const void* q,
+                                       const lowram_pages* pages, void* out, int32_t* sel_out,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+lowram_status lowram_decode_paged_workspace_size(const lowram_config* cfg, size_t* bytes);
+
 /* Read a run of tokens back out of the pages: k_out, v_out [n_seqs][n][H_kv][d] in cfg->dtype,
  * row i of sequence b is token start[b] + i (start NULL: 0) as code * scale, rounded to the
  * dtype (a scaled e4m3 code is exact in bf16 unless it is below bf16's normal range); rows

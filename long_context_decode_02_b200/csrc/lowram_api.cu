@@ -835,6 +835,21 @@ lowram_status check_pages(const lowram_pages* p, const lowram_config& c) {
   return LOWRAM_OK;
 }
 
+struct DecodePagedWs {
+  size_t out_f32, ml, paged, total;
+};
+DecodePagedWs decode_paged_ws(const lowram_config& c) {
+  const Dims dm = dims_of(c);
+  DecodePagedWs w{};
+  size_t o = align_up(decode_ws(c).total);
+  w.out_f32 = o; o = align_up(o + (size_t)dm.B * dm.Hq * dm.d * sizeof(float));
+  w.ml = o;      o = align_up(o + (size_t)dm.B * dm.Hq * 2 * sizeof(float));
+  w.paged = o;
+  o = align_up(o + paged_attend_workspace_bytes(dm.H, dm.G, dm.d, dm.dtype, dm.B, 1));
+  w.total = o;
+  return w;
+}
+
 PagedArgs paged_args(const lowram_ctx* ctx, const lowram_pages* p) {
   const lowram_config& c = ctx->cfg;
   PagedArgs a{};
@@ -924,6 +939,59 @@ lowram_status lowram_paged_attend(lowram_ctx* ctx, const lowram_pages* pages, co
   a.n_q = n_q;
   a.ws = workspace;
   if (launch_paged_attend(a, ctx->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    cudaGetLastError();
+    return LOWRAM_ERR_CUDA;
+  }
+  return LOWRAM_OK;
+}
+
+lowram_status lowram_decode_paged_workspace_size(const lowram_config* c, size_t* bytes) {
+  if (!bytes) return LOWRAM_ERR_INVALID_ARG;
+  const lowram_status st = lowram_check_config(c);
+  if (st != LOWRAM_OK) return st;
+  if (c->batch > kPagedMaxSeqs) return LOWRAM_ERR_UNSUPPORTED;
+  *bytes = decode_paged_ws(*c).total;
+  return LOWRAM_OK;
+}
+
+lowram_status lowram_decode_step_paged(lowram_ctx* ctx, const lowram_cache* cache,
+                                       const lowram_layer_params* params, const void* q,
+                                       const lowram_pages* pages, void* out, int32_t* sel_out,
+                                       void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ctx || !q || !out || !workspace) return LOWRAM_ERR_INVALID_ARG;
+  lowram_status st = check_layer_params(params);
+  if (st != LOWRAM_OK) return st;
+  if ((st = check_cache(cache, ctx->cfg)) != LOWRAM_OK) return st;
+  if ((st = check_pages(pages, ctx->cfg)) != LOWRAM_OK) return st;
+  if (pages->n_seqs != ctx->cfg.batch) return LOWRAM_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) ||
+      (sel_out && !aligned16(sel_out)))
+    return LOWRAM_ERR_ALIGN;
+  const DecodeWs w = decode_ws(ctx->cfg);
+  const DecodePagedWs pw = decode_paged_ws(ctx->cfg);
+  if (workspace_bytes < pw.total) return LOWRAM_ERR_WORKSPACE;
+  DeviceGuard g(ctx->device);
+  if (!g.ok) return LOWRAM_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  int32_t* sel = sel_out ? sel_out : reinterpret_cast<int32_t*>(ws + w.sel);
+  const bool tc = use_tc(ctx->cfg);
+  if ((st = select_impl(ctx, cache->landmark, cache->landmark_norm, q, sel, ws, w, s, tc)) !=
+      LOWRAM_OK)
+    return st;
+  float* const f32[2] = {reinterpret_cast<float*>(ws + pw.out_f32),
+                         reinterpret_cast<float*>(ws + pw.ml)};
+  if ((st = attend_impl(ctx, cache, params, q, sel, out, ws, w, s, tc, nullptr, f32)) !=
+      LOWRAM_OK)
+    return st;
+  PagedArgs a = paged_args(ctx, pages);
+  a.q = q;
+  a.out = out;
+  a.n_q = 1;
+  a.ws = ws + pw.paged;
+  a.pre_out = f32[0];
+  a.pre_ml = f32[1];
+  if (launch_paged_attend(a, ctx->num_sms, s) != cudaSuccess) {
     cudaGetLastError();
     return LOWRAM_ERR_CUDA;
   }

@@ -229,6 +229,9 @@ struct PagedArgs {
   // attend
   const void* q; void* out; float* lse; int n_q;
   void* ws;
+  // decode over a compressed prefix too: its normalised fp32 output [n_seqs][Hq][d] and softmax
+  // (max in natural-log units, sum) [n_seqs][Hq][2], merged with the pages' (n_q = 1), or null
+  const float* pre_out; const float* pre_ml;
   // gather
   const int32_t* start; int n; void* k_out; void* v_out;
 };

@@ -664,7 +664,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 // One CTA a query row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the partials
 // of its pair. The warps take every eighth partial with a running maximum each, so that all of a
 // row's loads are in flight together. Where the partials lie follows from the lengths; up to 32
-// sequences it is worked out while the first kernel runs.
+// sequences it is worked out while the first kernel runs. A compressed prefix joins as one more
+// partial.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const AttendParams p) {
   constexpr int E = D / 32, kW = kCombineThreads / 32, kStep = Tile<D>::kStep;
@@ -732,6 +733,14 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
   float M = -INFINITY, L = 0.f, w[kW];
 #pragma unroll
   for (int x = 0; x < kW; ++x) M = fmaxf(M, s_m[x]);
+  float pm = 0.f, pl = 0.f;   // a compressed prefix's softmax, max in log2 units
+  if (a.pre_ml) {
+    pm = a.pre_ml[2 * row] * 1.4426950408889634f;
+    pl = a.pre_ml[2 * row + 1];
+    M = fmaxf(M, pm);
+    pl *= exp2f(pm - M);
+    L = pl;
+  }
 #pragma unroll
   for (int x = 0; x < kW; ++x) {
     w[x] = s_m[x] == -INFINITY ? 1.f : exp2f(s_m[x] - M);
@@ -742,6 +751,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
     float o = 0.f;
 #pragma unroll
     for (int x = 0; x < kW; ++x) o = fmaf(w[x], s_o[x][threadIdx.x], o);
+    if (a.pre_ml) o = fmaf(a.pre_out[row * D + threadIdx.x], pl * kWeightScale, o);
     ((T*)a.out)[row * D + threadIdx.x] = from_f<T>(o * inv);
   }
   if (a.lse && threadIdx.x == 0)

@@ -124,6 +124,12 @@ _sig = {
                                  _P, ctypes.c_size_t, _P]),
     "lowram_paged_workspace_size": (_S, [ctypes.POINTER(lowram_config), ctypes.c_int32,
                                          ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)]),
+    "lowram_decode_step_paged": (_S, [_P, ctypes.POINTER(lowram_cache),
+                                      ctypes.POINTER(lowram_layer_params), _P,
+                                      ctypes.POINTER(lowram_pages), _P, _P, _P, ctypes.c_size_t,
+                                      _P]),
+    "lowram_decode_paged_workspace_size": (_S, [ctypes.POINTER(lowram_config),
+                                                ctypes.POINTER(ctypes.c_size_t)]),
     "lowram_paged_gather": (_S, [_P, ctypes.POINTER(lowram_pages), _P, ctypes.c_int32, _P, _P,
                                  _P]),
     "lowram_debug_reconstruct": (_S, [_P, ctypes.POINTER(lowram_cache),
@@ -579,3 +585,26 @@ def paged_gather(ctx: Context, pages: lowram_pages, k_out, v_out, start=None,
                              k_out.data_ptr(), v_out.data_ptr(), _paged_stream(ctx, stream))
     if st != OK:
         raise LowRAMError(st, "lowram_paged_gather")
+
+
+def decode_paged_workspace_size(cfg: lowram_config) -> int:
+    n = ctypes.c_size_t()
+    check(lowram_decode_paged_workspace_size(ctypes.byref(cfg), ctypes.byref(n)),
+          "lowram_decode_paged_workspace_size")
+    return n.value
+
+
+def decode_step_paged(ctx: Context, cache: dict, params: lowram_layer_params, q,
+                      pages: lowram_pages, out, workspace, sel_out=None, stream=None) -> None:
+    """lowram_decode_step_paged: decode over the compressed prefix plus the generated tokens in
+    a paged 8-bit cache, a suffix length of its own for every batch element."""
+    _paged_check(ctx, pages, q, out, workspace, sel_out)
+    shape = (ctx.cfg.batch, ctx.cfg.n_q_heads, ctx.cfg.head_dim)
+    dt = _float_dtype(ctx)
+    if tuple(q.shape) != shape or tuple(out.shape) != shape or q.dtype != dt or out.dtype != dt:
+        raise ValueError(f"q and out must be {dt} of shape {shape}")
+    cs = cache_struct(**cache)
+    check(lowram_decode_step_paged(ctx.handle, ctypes.byref(cs), ctypes.byref(params), _ptr(q),
+                                   pages._ref, _ptr(out), _ptr(sel_out), _ptr(workspace),
+                                   workspace.numel() * workspace.element_size(),
+                                   _paged_stream(ctx, stream)), "lowram_decode_step_paged")
