@@ -298,13 +298,15 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
     th64[i] = th;
     for (int t = 0; t < kRopeLo; ++t) {
       const double ang = (double)t * th;
-      lo64[(size_t)t * half + i] = make_double2(std::cos(ang), std::sin(ang));
-      lo32[(size_t)t * half + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
+      const double2 cs = make_double2(std::cos(ang), std::sin(ang));
+      lo64[(size_t)t * half + i] = cs;
+      lo32[(size_t)t * half + i] = make_float2((float)cs.x, (float)cs.y);
     }
     for (int j = 0; j < ctx->n_hi; ++j) {
       const double ang = (double)j * kRopeLo * th;
-      hi64[(size_t)j * half + i] = make_double2(std::cos(ang), std::sin(ang));
-      hi32[(size_t)j * half + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
+      const double2 cs = make_double2(std::cos(ang), std::sin(ang));
+      hi64[(size_t)j * half + i] = cs;
+      hi32[(size_t)j * half + i] = make_float2((float)cs.x, (float)cs.y);
     }
     for (size_t cc = 0; cc < n_chunks; ++cc) {
       const double ang = (double)(cc * (size_t)c->chunk) * th;

@@ -241,8 +241,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs 
   const lowram_pages& pg = a.pg;
   const int P = pg.page_tokens, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_launch_dependents();
   grid_dependency_wait();
+  grid_launch_dependents();
   const uint8_t* codes = (const uint8_t*)(blockIdx.z ? pg.v_code : pg.k_code);
   const float* scales = blockIdx.z ? pg.v_scale : pg.k_scale;
   T* out = (T*)(blockIdx.z ? a.v_out : a.k_out) + (size_t)b * a.n * a.H * D;

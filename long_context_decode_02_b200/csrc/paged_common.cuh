@@ -31,7 +31,8 @@ __device__ __forceinline__ uint32_t float4_to_e4m3x4(const float* x) {
 // The paged kernels are launched as programmatic dependents of whatever precedes them in the
 // stream: a kernel's blocks may be set up while the one before still runs, and touch memory only
 // behind grid_dependency_wait(), which returns when the kernels before have ended and their writes
-// are visible. (Back to back calls of an append and an attend: about 2 us less than plain
+// are visible. A kernel lets the next be set up only behind its own wait, so whatever the next one
+// does early sees everything older than its predecessor. (Back to back calls of an append and an attend: about 2 us less than plain
 // launches.)
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

@@ -51,3 +51,86 @@ def test_all_empty(L):
         assert ctx.last_error() == L.OK
         assert (out == 0).all() and torch.isneginf(lse).all()
         ctx.close()
+
+
+def test_pool_above_four_gigabytes(L):
+    """Pages whose byte offsets pass 32 bits behave as the same pages of a small pool."""
+    H, d, P, n = 8, 128, 64, 150
+    many = (1 << 32) // (H * P * d) + 40
+    ctx = context(L, "bf16", H, 2, d)
+    g = torch.Generator().manual_seed(3)
+    k, v = (torch.randn(n, H, d, generator=g).bfloat16().cuda() for _ in "kv")
+    q = torch.randn(1, 1, 2 * H, d, generator=g).bfloat16().cuda()
+    got = []
+    for n_pages, first in ((3, 0), (many, many - 3)):
+        t = L.alloc_pages(ctx.cfg, n_pages, P, "cuda")
+        table = torch.tensor([[first + 2, first, first + 1]], dtype=torch.int32, device="cuda")
+        lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        pages = L.paged_cache(t["k_code"], t["v_code"], t["k_scale"], t["v_scale"], table, lens)
+        L.paged_append(ctx, pages, k, v)
+        out, lse = torch.empty_like(q), torch.empty(1, 1, 2 * H, device="cuda")
+        ws = torch.empty(L.paged_workspace_size(ctx.cfg, 1), dtype=torch.uint8, device="cuda")
+        L.paged_attend(ctx, pages, q, out, ws, lse=lse)
+        ks, vs = (torch.empty(1, n, H, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        L.paged_gather(ctx, pages, ks, vs)
+        assert ctx.last_error() == L.OK
+        got.append((out, lse, ks, vs, t["k_scale"][first:first + 3].clone()))
+        del t, pages
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    ctx.close()
+
+
+def test_two_streams_at_once(L):
+    """One context, two streams, each with its own pages, outputs and workspace: the paged calls
+    keep nothing in the context."""
+    ctx = context(L, "bf16", 2, 4, 128)
+    runs = []
+    for i, lens in enumerate(([3000, 17, 900], [5000, 1, 0])):
+        c = Case(L, lens, 16, 2, 128, seed=40 + i)
+        pages = c.device()
+        q = torch.randn(3, 1, 8, 128, generator=torch.Generator().manual_seed(i)).bfloat16().cuda()
+        ws = torch.empty(L.paged_workspace_size(ctx.cfg, 3), dtype=torch.uint8, device="cuda")
+        alone = torch.empty_like(q)
+        L.paged_attend(ctx, pages, q, alone, ws)
+        runs.append((c, pages, q, ws, alone, torch.empty_like(q), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, pages, q, ws, alone, out, s in runs:
+            L.paged_attend(ctx, pages, q, out, ws, stream=s)
+    torch.cuda.synchronize()
+    assert ctx.last_error() == L.OK
+    for c, pages, q, ws, alone, out, s in runs:
+        assert torch.equal(alone, out)
+    ctx.close()
+
+
+def test_two_graphs_share_a_workspace(L):
+    """An append and an attend captured twice over one workspace, replayed in turns."""
+    ctx = context(L, "bf16", 2, 4, 64)
+    ws = torch.empty(L.paged_workspace_size(ctx.cfg, 2), dtype=torch.uint8, device="cuda")
+    made = []
+    for i in range(2):
+        c = Case(L, [40 + i, 700 * (i + 1)], 32, 2, 64, seed=50 + i)
+        pages = c.device()
+        q = torch.randn(2, 1, 8, 64, generator=torch.Generator().manual_seed(i)).bfloat16().cuda()
+        k = torch.randn(2, 2, 64, generator=torch.Generator().manual_seed(9 + i)).bfloat16().cuda()
+        out, want = torch.empty_like(q), torch.empty_like(q)
+
+        def step(o):
+            L.paged_append(ctx, pages, k, k)
+            L.paged_attend(ctx, pages, q, o, ws)
+
+        step(want)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step(out)
+        made.append((g, out, want, c, pages, q, k))
+    for _ in range(3):
+        for g, *_ in made:
+            g.replay()
+    torch.cuda.synchronize()
+    assert ctx.last_error() == L.OK
+    for g, out, want, *_ in made:
+        assert torch.equal(out, want)
+    ctx.close()
