@@ -29,8 +29,7 @@ struct lowram_ctx {
   int* item_ctr;  // device [H]: tile counters of the tcgen05 attend kernel, 0 between calls
   double* theta64;  // device [d/2]
   float2* chunk32;  // device [T/C][d/2]: (cos, sin)(c C theta_i)
-  double2* mid64;   // device [2^8][d/2], [2^7][d/2]: third RoPE level (RopeTables)
-  double2* top64;
+  double2* far64;   // device [3][32][d/2]: RoPE digits of far positions (RopeTables)
 };
 
 namespace {
@@ -147,8 +146,7 @@ RopeTables rope_of(const lowram_ctx* ctx) {
   r.half = ctx->cfg.head_dim / 2;
   r.theta64 = ctx->theta64;
   r.chunk32 = ctx->chunk32;
-  r.mid64 = ctx->mid64;
-  r.top64 = ctx->top64;
+  r.far64 = ctx->far64;
   return r;
 }
 
@@ -291,8 +289,8 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
   std::vector<double> th64((size_t)half);
   const size_t n_chunks = (size_t)(n_pos / c->chunk);
   std::vector<float2> chunk32(n_chunks * half);
-  constexpr int kMid = 1 << kRopeMidBits, kTop = 1 << kRopeTopBits;
-  std::vector<double2> mid64((size_t)half * kMid), top64((size_t)half * kTop);
+  constexpr int kFar = 1 << kRopeFarBits;
+  std::vector<double2> far64((size_t)half * kFar * kRopeFarLevels);
   for (int i = 0; i < half; ++i) {
     const double th = std::pow(c->rope_theta, -2.0 * i / c->head_dim);
     th64[i] = th;
@@ -312,14 +310,11 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
       const double ang = (double)(cc * (size_t)c->chunk) * th;
       chunk32[cc * half + i] = make_float2((float)std::cos(ang), (float)std::sin(ang));
     }
-    for (int j = 0; j < kMid; ++j) {
-      const double ang = (double)(j << kRopeLoBits) * th;
-      mid64[(size_t)j * half + i] = make_double2(std::cos(ang), std::sin(ang));
-    }
-    for (int j = 0; j < kTop; ++j) {
-      const double ang = (double)(j << (kRopeLoBits + kRopeMidBits)) * th;
-      top64[(size_t)j * half + i] = make_double2(std::cos(ang), std::sin(ang));
-    }
+    for (int l = 0; l < kRopeFarLevels; ++l)
+      for (int j = 0; j < kFar; ++j) {
+        const double ang = (double)(j << (kRopeLoBits + kRopeFarBits * l)) * th;
+        far64[(size_t)(kFar * l + j) * half + i] = make_double2(std::cos(ang), std::sin(ang));
+      }
   }
   const size_t pairs = (size_t)c->batch * c->n_kv_heads;
   bool ok = cudaMalloc(&ctx->lo32, lo32.size() * sizeof(float2)) == cudaSuccess &&
@@ -333,8 +328,7 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
             cudaMalloc(&ctx->scores, pairs * (size_t)(c->n_tokens / c->chunk) * sizeof(float)) == cudaSuccess &&
             cudaMalloc(&ctx->theta64, th64.size() * sizeof(double)) == cudaSuccess &&
             cudaMalloc(&ctx->chunk32, chunk32.size() * sizeof(float2)) == cudaSuccess &&
-            cudaMalloc(&ctx->mid64, mid64.size() * sizeof(double2)) == cudaSuccess &&
-            cudaMalloc(&ctx->top64, top64.size() * sizeof(double2)) == cudaSuccess;
+            cudaMalloc(&ctx->far64, far64.size() * sizeof(double2)) == cudaSuccess;
   ok = ok &&
        cudaMemcpy(ctx->lo32, lo32.data(), lo32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
        cudaMemcpy(ctx->hi32, hi32.data(), hi32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
@@ -347,8 +341,7 @@ lowram_status lowram_create(const lowram_config* c, int device, lowram_ctx** out
        cudaMemset(ctx->scores, 0xff, pairs * (size_t)(c->n_tokens / c->chunk) * sizeof(float)) == cudaSuccess &&
        cudaMemcpy(ctx->theta64, th64.data(), th64.size() * sizeof(double), cudaMemcpyHostToDevice) == cudaSuccess &&
        cudaMemcpy(ctx->chunk32, chunk32.data(), chunk32.size() * sizeof(float2), cudaMemcpyHostToDevice) == cudaSuccess &&
-       cudaMemcpy(ctx->mid64, mid64.data(), mid64.size() * sizeof(double2), cudaMemcpyHostToDevice) == cudaSuccess &&
-       cudaMemcpy(ctx->top64, top64.data(), top64.size() * sizeof(double2), cudaMemcpyHostToDevice) == cudaSuccess;
+       cudaMemcpy(ctx->far64, far64.data(), far64.size() * sizeof(double2), cudaMemcpyHostToDevice) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
     lowram_destroy(ctx);
@@ -372,8 +365,7 @@ void lowram_destroy(lowram_ctx* ctx) {
   cudaFree(ctx->item_ctr);
   cudaFree(ctx->theta64);
   cudaFree(ctx->chunk32);
-  cudaFree(ctx->mid64);
-  cudaFree(ctx->top64);
+  cudaFree(ctx->far64);
   delete ctx;
 }
 

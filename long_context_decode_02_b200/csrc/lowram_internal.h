@@ -35,14 +35,12 @@ struct RopeTables {
   // chunk-base rotations: chunk32[c * half + i] = (cos, sin)(c C theta_i), c < T / C,
   // from fp64 on the host
   const float2* chunk32;
-  // third level, for positions behind the prefix (any position < 2^24 = top, mid, lo bits):
-  //   mid64[j * half + i] = (cos, sin)(j 2^9 theta_i), j < 2^8
-  //   top64[j * half + i] = (cos, sin)(j 2^17 theta_i), j < 2^7
-  const double2* mid64;
-  const double2* top64;
+  // for any position < 2^24, also behind the prefix: three digits of 5 bits above the low 9,
+  //   far64[(32 l + j) * half + i] = (cos, sin)(j 2^(9 + 5 l) theta_i), l < 3, j < 32
+  const double2* far64;
 };
-constexpr int kRopeMidBits = 8, kRopeTopBits = 7;
-constexpr int kMaxPosition = 1 << (kRopeLoBits + kRopeMidBits + kRopeTopBits);
+constexpr int kRopeFarBits = 5, kRopeFarLevels = 3;
+constexpr int kMaxPosition = 1 << (kRopeLoBits + kRopeFarBits * kRopeFarLevels);
 
 struct Dims {
   int B, T, H, Hq, G, d, r, C, F, Nc, k, n_res, act, dtype;

@@ -11,7 +11,7 @@
 // Bound by bytes: 2 N H d (es + 1). A warp takes 16 rows of one page and head, keys or values; the
 // 1, 2 or 4 warps of a (page, head) agree on its maximum. A lane holds the same two pairs (four
 // elements) of each of its rows in registers, so the input is read once, and turns its (cos, sin)
-// on from row to row by theta_i: one look-up (three table levels) a warp, four fp64 operations a
+// on from row to row by theta_i: one look-up (four table levels) a warp, four fp64 operations a
 // row and pair, no shared memory. Angles and products are fp64 because e4m3's rounding and the
 // scale's power of two are decisions: an fp32 rotation would flip one in about 2^20 of them
 // against the formula. Short-lived CTAs, five an SM, keep the loads in flight; a CTA that went
@@ -28,13 +28,19 @@ constexpr int kThreads = 256;        // gather
 constexpr int kAppendThreads = 128;
 constexpr int kRowsPerWarp = 16;
 
+__device__ __forceinline__ double2 turn(double2 c, double2 d) {   // angles added
+  return make_double2(c.x * d.x - c.y * d.y, c.y * d.x + c.x * d.y);
+}
 // (cos, sin)(pos * theta_i), pos < 2^24
 __device__ __forceinline__ double2 rope_any64(const RopeTables& rt, int i, int pos) {
-  const double2 lo = rt.lo64[(pos & (kRopeLo - 1)) * rt.half + i];
-  const double2 mi = rt.mid64[((pos >> kRopeLoBits) & ((1 << kRopeMidBits) - 1)) * rt.half + i];
-  const double2 to = rt.top64[(pos >> (kRopeLoBits + kRopeMidBits)) * rt.half + i];
-  const double2 hi = make_double2(to.x * mi.x - to.y * mi.y, to.y * mi.x + to.x * mi.y);
-  return make_double2(hi.x * lo.x - hi.y * lo.y, hi.y * lo.x + hi.x * lo.y);
+  constexpr int kFar = 1 << kRopeFarBits;
+  double2 c = rt.lo64[(pos & (kRopeLo - 1)) * rt.half + i], f[kRopeFarLevels];
+#pragma unroll
+  for (int l = 0; l < kRopeFarLevels; ++l)
+    f[l] = rt.far64[(kFar * l + ((pos >> (kRopeLoBits + kRopeFarBits * l)) & (kFar - 1))) * rt.half + i];
+#pragma unroll
+  for (int l = 0; l < kRopeFarLevels; ++l) c = turn(c, f[l]);
+  return c;
 }
 
 // exponent e of the smallest 2^e, e >= -64, with amax <= 448 * 2^e (448 = 1.75 * 2^8)
@@ -55,10 +61,6 @@ template <> struct Two<float> {
   using Raw = float2;
   static __device__ __forceinline__ float2 get(Raw r) { return r; }
 };
-
-__device__ __forceinline__ double2 turn(double2 c, double2 d) {   // angles added
-  return make_double2(c.x * d.x - c.y * d.y, c.y * d.x + c.x * d.y);
-}
 
 // grid (units of a sequence / teams, n_seqs, 2): a unit is a (page, head), a team the warps of one.
 // Lane l: pairs 2 (l % LR), + 1 of rows l / LR + RS k.
@@ -111,6 +113,7 @@ paged_append_kernel(const PagedArgs a) {
   const int wrow = (warp % wt) * kRowsPerWarp;   // the warp's rows wrow .. wrow + 15
   const bool any = mine && wrow < hi && wrow + kRowsPerWarp > lo;
   const bool all = any && wrow >= lo && wrow + kRowsPerWarp <= hi;
+  int page = mine ? pg.table[(size_t)b * pg.max_pages + pi] : -1;   // looked at further below
   float x[NR][4];   // pair i0's first and second element, pair i0 + 1's
   float amax = 0.f;
   // ROT: rotated keys. ALL: every row of the warp is new, as in all pages of a long prompt but
@@ -187,9 +190,12 @@ paged_append_kernel(const PagedArgs a) {
       }
     }
   }
-  const int page = mine ? paged_page(pg, b, pi, a.status) : -1;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (mine && (page < 0 || page >= pg.n_pages)) {
+    raise_status(a.status, kStatusDeviceCheck);
+    page = -1;
+  }
   const size_t ph = (size_t)(page < 0 ? 0 : page) * a.H + h;
   const float old = page >= 0 && lo > 0 ? scales[ph] : 0.f;
   if (wt > 1) {   // the team's maximum; everyone has read the old scale before it is replaced
