@@ -119,6 +119,10 @@ ATTEND = [
     ("f32", 2, 4, 128, 32, 4, [3, 4, 90]),
     ("f32", 1, 2, 64, 16, 16, [20, 129]),
     ("bf16", 4, 4, 128, 16, 1, list(range(0, 66, 5))),
+    ("bf16", 2, 8, 64, 32, 5, [4, 77, 600]),                # 40 rows a head: groups of 24
+    ("bf16", 2, 2, 128, 64, 11, [10, 300]),
+    ("bf16", 1, 4, 128, 16, 6, [0, 5, 47, 48, 49]),
+    ("bf16", 2, 4, 64, 16, 4, [33, 2, 260]),                # 16 rows
 ]
 
 
