@@ -662,8 +662,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 }
 
 // One CTA a query row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the partials
-// of its pair. The warps take every eighth partial with a running maximum each, so that all of a
-// row's loads are in flight together. Where the partials lie follows from the lengths; up to 32
+// of its pair. The warps take every eighth partial, four of them in flight together (one after
+// another, the 129 partials of a 4K sequence took 6 us). Where the partials lie follows from the lengths; up to 32
 // sequences it is worked out while the first kernel runs. A compressed prefix joins as one more
 // partial.
 template <typename T, int D>
@@ -691,9 +691,9 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
     ns = (int)(p.ws.first[b + 1] - before);
   }
   const int share = run_steps(total * pairs, p.n_warps);
-  const long long s0 = before * pairs + (long long)pair * ns;
-  const int first = (int)div_pos(s0, share);
-  const int count = ns > 0 ? (int)div_pos(s0 + ns - 1, share) - first + 1 : 0;
+  const long long step0 = before * pairs + (long long)pair * ns;
+  const int first = (int)div_pos(step0, share);
+  const int count = ns > 0 ? (int)div_pos(step0 + ns - 1, share) - first + 1 : 0;
   const size_t slot0 = (size_t)first + (size_t)b * pairs + pair;
   const float2* ml = p.ws.ml + slot0 * p.rp.rows + rg;
   const float* po = p.ws.o + (slot0 * p.rp.rows + rg) * D + lane * E;
@@ -703,24 +703,42 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int s = warp; s < count; s += kW) {
-    const float2 x = ml[(size_t)s * p.rp.rows];
-    float o[E];
-    if constexpr (E == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(po + s * so);
-      o[0] = y.x; o[1] = y.y; o[2] = y.z; o[3] = y.w;
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(po + s * so);
-      o[0] = y.x; o[1] = y.y;
-    }
-    const float mn = fmaxf(m, x.x);
-    // a partial that saw nothing holds zeros; a NaN sum must stay one
-    const float c = m == -INFINITY ? 1.f : exp2f(m - mn);
-    const float w = x.x == -INFINITY ? 1.f : exp2f(x.x - mn);
-    m = mn;
-    l = fmaf(l, c, w * x.y);
+  constexpr int kU = 4;   // partials of a warp in flight together
+  for (int s0 = warp; s0 < count; s0 += kU * kW) {
+    float2 x[kU];
+    float o[kU][E], mn = m;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(acc[e], c, w * o[e]);
+    for (int u = 0; u < kU; ++u) {
+      const int s = s0 + u * kW;
+      x[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[u][e] = 0.f;
+      if (s < count) {
+        x[u] = ml[(size_t)s * p.rp.rows];
+        if constexpr (E == 4) {
+          const float4 y = *reinterpret_cast<const float4*>(po + s * so);
+          o[u][0] = y.x; o[u][1] = y.y; o[u][2] = y.z; o[u][3] = y.w;
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(po + s * so);
+          o[u][0] = y.x; o[u][1] = y.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) mn = fmaxf(mn, x[u].x);
+    // what saw nothing holds zeros; a NaN sum must stay one
+    const float c = m == -INFINITY ? 1.f : ex2_approx(m - mn);
+    m = mn;
+    l *= c;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= c;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const float w = x[u].x == -INFINITY ? 1.f : ex2_approx(x[u].x - mn);
+      l = fmaf(w, x[u].y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, o[u][e], acc[e]);
+    }
   }
   __shared__ float s_m[kW], s_l[kW], s_o[kW][D];
   if (lane == 0) {
@@ -738,12 +756,12 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
     pm = a.pre_ml[2 * row] * 1.4426950408889634f;
     pl = a.pre_ml[2 * row + 1];
     M = fmaxf(M, pm);
-    pl *= exp2f(pm - M);
+    pl *= ex2_approx(pm - M);
     L = pl;
   }
 #pragma unroll
   for (int x = 0; x < kW; ++x) {
-    w[x] = s_m[x] == -INFINITY ? 1.f : exp2f(s_m[x] - M);
+    w[x] = s_m[x] == -INFINITY ? 1.f : ex2_approx(s_m[x] - M);
     L = fmaf(w[x], s_l[x], L);
   }
   const float inv = L == 0.f ? 0.f : 1.f / (L * kWeightScale);
