@@ -30,9 +30,9 @@
 // eight times finer than the bf16 output), for fp32 again in two columns (2^-22). The matrix
 // unit cuts its sums toward zero, so fp32 contexts start each step's product from zero and add it
 // to the output in fp32: a cut of 2^-24 for each of a run's thousands of tokens is a bias of 1e-6.
-// Values carry their page's scale s_v = fr 2^ev inside the weight: the reference of a row is
-// max(z + ev) over its tokens, so
-//   a = 2^(z + ev - m) <= 1,  weight = a fr 2^13,  sum += a 2^-ev,
+// Values carry their page's scale s_v = fr 2^ev inside the weight: the reference m of a row is
+// max(z + ev) over its tokens to within 2^6, so
+//   a = 2^(z + ev - m) <= 2^6,  weight = a fr 2^8 < 2^15,  sum += a 2^-ev,
 // and pages whose scales lie far apart cost each other no digits.
 #include <cuda.h>
 
@@ -52,7 +52,8 @@ constexpr int kStages = 2;                // a warp's ring: 16 KB
 constexpr uint32_t kHalfBytes = 4096;     // K (or V) of a step
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kRingBytes = kStages * kStageBytes;
-constexpr float kWeightScale = 8192.f;    // 2^13: weights in fp16 stay normal down to 2^-27
+constexpr float kWeightScale = 256.f;     // 2^8: weights in fp16 stay normal down to 2^-22
+constexpr float kSlack = 6.f;             // log2 of what a weight may exceed its reference by
 constexpr int kCombineThreads = 256;
 
 template <int D> struct Tile {
@@ -184,7 +185,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
   constexpr int kC = D / 16, kOT = D / 16;          // 16-byte chunks of a row
   constexpr int NT = F32 ? RL : (RL + 1) / 2;       // column tiles
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, fr 2^13, ev, valid tokens
+  __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, fr 2^8, ev, valid tokens
   __shared__ int4 s_desc[kWarps][S];        // a stage's step: sequence, pair, first token, length
   __shared__ int2 s_part[kWarps][S];        // its partial; 1: begins one, 2: ends it
   __shared__ int s_nan[kWarps][D];          // first token with a NaN value that not all rows see
@@ -535,7 +536,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         __syncwarp();
         fence_proxy_async_smem();   // before a copy fills the stage again
       }
-      // reference: max of z + ev
+      // reference: the max of z + ev, moved only when a token exceeds it by 2^kSlack: few steps
+      // then pay for the reduction over the lanes and the output's rescaling
       float ev[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) ev[u] = (float)__float_as_int(meta[u].z);
@@ -543,21 +545,20 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
       bool grow = false;
 #pragma unroll
       for (int x = 0; x < RL; ++x) {
-        float v = fmaxf(z[0][x][0], z[0][x][1]) + ev[0];
+        mn[x] = fmaxf(z[0][x][0], z[0][x][1]) + ev[0];
 #pragma unroll
-        for (int u = 1; u < U; ++u) v = fmaxf(v, fmaxf(z[u][x][0], z[u][x][1]) + ev[u]);
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        mn[x] = fmaxf(m[x], v);
-        grow = grow || mn[x] > m[x];
+        for (int u = 1; u < U; ++u) mn[x] = fmaxf(mn[x], fmaxf(z[u][x][0], z[u][x][1]) + ev[u]);
+        grow = grow || mn[x] > m[x] + kSlack;
       }
       if (__any_sync(0xffffffffu, grow)) {
         float corr[RL];
 #pragma unroll
         for (int x = 0; x < RL; ++x) {
-          corr[x] = mn[x] > m[x] ? ex2_approx(m[x] - mn[x]) : 1.f;
-          m[x] = mn[x];
+          float v = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 4));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          corr[x] = v > m[x] ? ex2_approx(m[x] - v) : 1.f;
+          m[x] = fmaxf(m[x], v);
           l[x] *= corr[x];
         }
 #pragma unroll

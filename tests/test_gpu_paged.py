@@ -204,6 +204,34 @@ def test_attend_value_scales_apart(L):
             ctx.close()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("slope", [0.02, 0.11, 0.5, -0.11])
+def test_attend_rising_logits(L, dtype, d, slope):
+    """Logits that rise (or fall) steadily along the sequence, by a little or by far more than a
+    reference's slack every few tokens."""
+    n = 700
+    c = Case(L, [n], 16, 1, d, seed=15, spread=1)
+    order = c.table[0, :-(-n // 16)]
+    t = np.arange(len(order) * 16, dtype=np.float64).reshape(-1, 16)
+    k = np.zeros((c.n_pages, 1, 16, d))
+    k[order, 0, :, 0] = np.floor(t * slope * 16) / 16 % 256     # what the 8-bit value leaves is in element 1
+    k[order, 0, :, 1] = np.floor(t * slope * 16) / 16 // 256 * 256
+    c.ref.code["k"] = R.encode(np.clip(k, -448, 448))
+    c.ref.scale["k"][:] = 1.0
+    pages = c.device()
+    ctx = context(L, dtype, 1, 2, d)
+    q = torch.zeros(1, 1, 2, d)
+    q[..., 0] = q[..., 1] = d ** 0.5
+    q[:, :, 1, 2:] = torch.randn(d - 2, generator=torch.Generator().manual_seed(1)) * 0.1
+    q = q.to(DT[dtype]).cuda()
+    out, lse = torch.empty_like(q), torch.empty(1, 1, 2, device="cuda")
+    ws = torch.empty(L.paged_workspace_size(ctx.cfg, 1), dtype=torch.uint8, device="cuda")
+    L.paged_attend(ctx, pages, q, out, ws, lse=lse)
+    assert ctx.last_error() == L.OK
+    check_attend(dtype, out, lse, c.ref.attend(c.table, c.lens, f64(q), 2))
+    ctx.close()
+
+
 def test_attend_nan_only_reaches_its_rows(L):
     """A NaN key of a valid token reaches the rows that see it and no others."""
     c = Case(L, [40, 40], 16, 1, 128, seed=13)
