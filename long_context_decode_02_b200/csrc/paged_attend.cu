@@ -505,29 +505,27 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
               const int tk = s_token(g + 8 * k);
               if (tk >= valid || tok0 + u * kUnit + tk >= lim[x]) z[u][x][k] = -INFINITY;
             }
-          for (int r = 0; r < kUnit; ++r) {
-            const int row = u * kUnit + r, tk = tok0 + row;
+          // rows from `valid` on lie together
+          for (uint32_t o = (u * kUnit + valid) * D + 16 * lane; o < (u + 1) * kUnit * D; o += 512)
+            st_shared_v4(vb + o, 0, 0, 0, 0);
+          // Tokens that only some rows see: their NaN codes would reach the others as 0 * NaN, so
+          // they become zeros here and the first of each element is kept for the end.
+          for (int row = max(vis - tok0, u * kUnit); row < u * kUnit + valid; ++row) {
             uint8_t* bytes = smem_raw + (vb - smem_u32(smem_raw)) + row * D;
-            if (r >= valid) {
-              if (lane < D / 4) reinterpret_cast<uint32_t*>(bytes)[lane] = 0;
-            } else if (tk >= vis) {
-              // a token that only some rows see: its NaN codes would reach the others as 0 * NaN,
-              // so they become zeros here and the first of each element is kept for the end
 #pragma unroll
-              for (int e = lane; e < D; e += 32) {
-                const bool nan = (bytes[e] & 127) == 127;
-                if (__any_sync(0xffffffffu, nan)) {
-                  if (!poison) {
-                    poison = true;
-                    for (int y = lane; y < D; y += 32) s_nan[warp][y] = 0x7fffffff;
-                    __syncwarp();
-                  }
-                  // the element behind byte e: the chunk's swizzle undone (it is its own inverse)
-                  const int el = (int)(chunk_offset<D>(row, e >> 4) - row * D) + (e & 15);
-                  if (nan) {
-                    s_nan[warp][el] = min(s_nan[warp][el], tk);
-                    bytes[e] = 0;
-                  }
+            for (int e = lane; e < D; e += 32) {
+              const bool nan = (bytes[e] & 127) == 127;
+              if (__any_sync(0xffffffffu, nan)) {
+                if (!poison) {
+                  poison = true;
+                  for (int y = lane; y < D; y += 32) s_nan[warp][y] = 0x7fffffff;
+                  __syncwarp();
+                }
+                // the element behind byte e: the chunk's swizzle undone (it is its own inverse)
+                const int el = (int)(chunk_offset<D>(row, e >> 4) - row * D) + (e & 15);
+                if (nan) {
+                  s_nan[warp][el] = min(s_nan[warp][el], tok0 + row);
+                  bytes[e] = 0;
                 }
               }
             }

@@ -454,6 +454,10 @@ def paged_cache(k_code, v_code, k_scale, v_scale, table, lens) -> lowram_pages:
     p._ref = ctypes.byref(p)
     p._heads = (k_code.shape[1], k_code.shape[3])
     p._device = k_code.get_device()
+    # what the calls below look up every time
+    p._dtype = {DTYPE_BF16: torch.bfloat16, DTYPE_F32: torch.float32}
+    p._int32, p._float32 = torch.int32, torch.float32
+    p._raw_stream = torch._C._cuda_getCurrentRawStream
     return p
 
 
@@ -473,25 +477,16 @@ def _paged_check(ctx: Context, pages: lowram_pages, *tensors) -> None:
                 raise ValueError(f"tensor of shape {tuple(t.shape)} is not contiguous")
 
 
-def _paged_stream(ctx: Context, stream):
+def _paged_stream(ctx: Context, pages: lowram_pages, stream):
     """The given stream, or the current one of the context's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    return torch._C._cuda_getCurrentRawStream(ctx.device)
+    return stream.cuda_stream if stream is not None else pages._raw_stream(ctx.device)
 
 
-def _float_dtype(ctx: Context):
-    import torch
-    return torch.bfloat16 if ctx.cfg.dtype == DTYPE_BF16 else torch.float32
-
-
-def _int32(t, n: int, name: str):
+def _int32(pages: lowram_pages, t, n: int, name: str):
     """Device address of an optional [n] int32 array."""
     if t is None:
         return None
-    import torch
-    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+    if t.dtype != pages._int32 or t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must be int32 of shape ({n},), got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -511,7 +506,7 @@ def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, m
     shape = k_new.shape
     if shape != v_new.shape or len(shape) not in (3, 4) or shape[-2] != H or shape[-1] != d:
         raise ValueError(f"k_new and v_new must be [n_new][{H}][{d}]")
-    dt = _float_dtype(ctx)
+    dt = pages._dtype[ctx.cfg.dtype]
     if k_new.dtype != dt or v_new.dtype != dt:
         raise ValueError(f"k_new and v_new must be {dt}")
     if len(shape) == 4:
@@ -530,10 +525,10 @@ def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, m
                 ks, vs = a[0], b[0]
     n_seqs = pages.n_seqs
     st = lowram_paged_append(ctx._h, pages._ref, k_new.data_ptr(), v_new.data_ptr(), ks, vs, n,
-                             _int32(cu_new, n_seqs + 1, "cu_new"),
+                             _int32(pages, cu_new, n_seqs + 1, "cu_new"),
                              n if max_new is None else max_new,
-                             _int32(pos_base, n_seqs, "pos_base"), 1 if rotate else 0,
-                             _paged_stream(ctx, stream))
+                             _int32(pages, pos_base, n_seqs, "pos_base"), 1 if rotate else 0,
+                             _paged_stream(ctx, pages, stream))
     if st != OK:
         raise LowRAMError(st, "lowram_paged_append")
 
@@ -549,9 +544,8 @@ def paged_attend(ctx: Context, pages: lowram_pages, q, out, workspace, lse=None,
                  stream=None) -> None:
     """lowram_paged_attend: attention of q [n_seqs][n_q][H_q][d] (or [n_seqs][H_q][d]: one
     query a sequence) over the pages; out like q, lse [n_seqs][n_q][H_q] fp32."""
-    import torch
     _paged_check(ctx, pages, q, out, workspace, lse)
-    dt = _float_dtype(ctx)
+    dt = pages._dtype[ctx.cfg.dtype]
     shape = q.shape
     if (len(shape) not in (3, 4) or shape[0] != pages.n_seqs or shape[-2] != ctx.cfg.n_q_heads or
             shape[-1] != pages._heads[1] or out.shape != shape):
@@ -559,12 +553,12 @@ def paged_attend(ctx: Context, pages: lowram_pages, q, out, workspace, lse=None,
                          f"[{pages._heads[1]}]")
     if q.dtype != dt or out.dtype != dt:
         raise ValueError(f"q and out must be {dt}")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:-1]):
+    if lse is not None and (lse.dtype != pages._float32 or lse.shape != shape[:-1]):
         raise ValueError(f"lse must be fp32 of shape {tuple(shape[:-1])}")
     st = lowram_paged_attend(ctx._h, pages._ref, q.data_ptr(), shape[1] if len(shape) == 4 else 1,
                              out.data_ptr(), None if lse is None else lse.data_ptr(),
                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                             _paged_stream(ctx, stream))
+                             _paged_stream(ctx, pages, stream))
     if st != OK:
         raise LowRAMError(st, "lowram_paged_attend")
 
@@ -578,11 +572,11 @@ def paged_gather(ctx: Context, pages: lowram_pages, k_out, v_out, start=None,
     if (len(shape) != 4 or shape[0] != pages.n_seqs or
             (shape[2], shape[3]) != pages._heads or v_out.shape != shape):
         raise ValueError(f"k_out and v_out must be [{pages.n_seqs}][n][H, d = {pages._heads}]")
-    dt = _float_dtype(ctx)
+    dt = pages._dtype[ctx.cfg.dtype]
     if k_out.dtype != dt or v_out.dtype != dt:
         raise ValueError(f"k_out and v_out must be {dt}")
-    st = lowram_paged_gather(ctx._h, pages._ref, _int32(start, pages.n_seqs, "start"), shape[1],
-                             k_out.data_ptr(), v_out.data_ptr(), _paged_stream(ctx, stream))
+    st = lowram_paged_gather(ctx._h, pages._ref, _int32(pages, start, pages.n_seqs, "start"), shape[1],
+                             k_out.data_ptr(), v_out.data_ptr(), _paged_stream(ctx, pages, stream))
     if st != OK:
         raise LowRAMError(st, "lowram_paged_gather")
 
@@ -600,11 +594,11 @@ def decode_step_paged(ctx: Context, cache: dict, params: lowram_layer_params, q,
     a paged 8-bit cache, a suffix length of its own for every batch element."""
     _paged_check(ctx, pages, q, out, workspace, sel_out)
     shape = (ctx.cfg.batch, ctx.cfg.n_q_heads, ctx.cfg.head_dim)
-    dt = _float_dtype(ctx)
+    dt = pages._dtype[ctx.cfg.dtype]
     if tuple(q.shape) != shape or tuple(out.shape) != shape or q.dtype != dt or out.dtype != dt:
         raise ValueError(f"q and out must be {dt} of shape {shape}")
     cs = cache_struct(**cache)
     check(lowram_decode_step_paged(ctx.handle, ctypes.byref(cs), ctypes.byref(params), _ptr(q),
                                    pages._ref, _ptr(out), _ptr(sel_out), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(),
-                                   _paged_stream(ctx, stream)), "lowram_decode_step_paged")
+                                   _paged_stream(ctx, pages, stream)), "lowram_decode_step_paged")
