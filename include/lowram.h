@@ -301,7 +301,8 @@ lowram_status lowram_append(lowram_ctx* dst_ctx, const lowram_cache* dst,
  * page_tokens is 16, 32 or 64; n_pages * H_kv * page_tokens < 2^31 and max_pages * page_tokens
  * <= 2^24 (LOWRAM_ERR_UNSUPPORTED otherwise); n_seqs 1 .. 8192, independent of the context's
  * batch. Of the context the calls use n_kv_heads, n_q_heads, head_dim, dtype (fp32 or bf16),
- * rope_theta and the device. Sequences may share pages that are only read; a page that an
+ * rope_theta and the device; they keep nothing in it between calls, so they may overlap on
+ * several streams, each with a workspace of its own. Sequences may share pages that are only read; a page that an
  * append writes belongs to one sequence (not checked: the rows of the other sequence are then
  * overwritten).
  * Lengths and page indices are read on the device. A length outside 0 .. max_pages *

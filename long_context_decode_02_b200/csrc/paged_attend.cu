@@ -11,7 +11,8 @@
 //
 // Two stages a warp, not three: with 192 KB of an SM always asked for, four groups of ten SMs get
 // a tenth less of the bandwidth than the others and end that much later (batch 8 at 128K tokens:
-// SMs end at 280 .. 350 us); with 128 KB all get the same (300 .. 319 us; the call 354 -> 326 us).
+// SMs end at 280 .. 350 us); with 128 KB all get the same (300 .. 319 us; the call 354 -> 326 us,
+// now 320, 6.7 TB/s; over caches that find nothing in the L2 328 .. 341).
 // Handing the list's end out in short runs instead cost more than it evened out (a run's queries,
 // partial and pages are about 3 us of a warp).
 //
@@ -80,8 +81,8 @@ inline RowPlan row_plan(int G, int n_q, int dtype) {
 }
 
 // Workspace: first step of every sequence (of one pair each) and their total, for the merge of
-// more than 32 sequences; the partials' (m, l) and outputs. The partial of warp w for pair x (= (b H + h)
-// groups + group) is number w + x: both only grow along the list of steps.
+// more than 32 sequences; the partials' (m, l) and outputs. The partial of warp w for pair x
+// (= (b H + h) groups + group) is number w + x: both only grow along the list of steps.
 struct AttendWs {
   long long* first;   // [n_seqs + 1]
   float2* ml;   // [slots][rows]
@@ -314,6 +315,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
       raise_status(a.status, kStatusDeviceCheck);
       nvalid = 0;
     }
+    nsk = nsv = 0.f;   // no unit: a stale scale, were it NaN, would reach masked weights as 0 * NaN
     if (nvalid > 0) {
       const size_t ph = (size_t)npage * a.H + npair / p.rp.groups;
       nsk = pg.k_scale[ph];
@@ -662,9 +664,9 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 
 // One CTA a query row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the partials
 // of its pair. The warps take every eighth partial, four of them in flight together (one after
-// another, the 129 partials of a 4K sequence took 6 us). Where the partials lie follows from the lengths; up to 32
-// sequences it is worked out while the first kernel runs. A compressed prefix joins as one more
-// partial.
+// another, the 129 partials of a 4K sequence took 6 us). Where the partials lie follows from the
+// lengths; up to 32 sequences it is worked out while the first kernel runs. A compressed prefix
+// joins as one more partial.
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const AttendParams p) {
   constexpr int E = D / 32, kW = kCombineThreads / 32, kStep = Tile<D>::kStep;

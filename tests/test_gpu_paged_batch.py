@@ -134,3 +134,52 @@ def test_two_graphs_share_a_workspace(L):
     for g, out, want, *_ in made:
         assert torch.equal(out, want)
     ctx.close()
+
+
+def test_nan_scale_stays_in_its_sequence(L):
+    """A sequence with NaN scales (a cache written elsewhere, or never) reaches no other one that the
+    same warps take."""
+    lens = [16, 20, 16, 40] * 500          # short runs of many sequences in every warp
+    c = Case(L, lens, 16, 1, 64, seed=60)
+    for b in range(0, len(lens), 4):
+        c.ref.scale["v"][c.table[b, 0]] = np.nan
+        c.ref.scale["k"][c.table[b, 0]] = np.nan
+    pages = c.device()
+    ctx = context(L, "bf16", 1, 2, 64)
+    q = torch.randn(len(lens), 1, 2, 64, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    out = torch.empty_like(q)
+    ws = torch.empty(L.paged_workspace_size(ctx.cfg, len(lens)), dtype=torch.uint8, device="cuda")
+    L.paged_attend(ctx, pages, q, out, ws)
+    assert ctx.last_error() == L.OK
+    nan = torch.isnan(out).flatten(1).any(dim=1).cpu()
+    assert nan[0::4].all() and not nan[1::4].any() and not nan[2::4].any() and not nan[3::4].any()
+    ctx.close()
+
+
+def test_oversize_pools_are_refused(L):
+    """Sizes whose rows or positions pass the kernels' indices, by descriptor only."""
+    import ctypes
+    c = Case(L, [20], 16, 8, 128, seed=61)
+    pages = c.device()
+    ctx = context(L, "bf16", 8, 1, 128)
+    q = torch.zeros(1, 1, 8, 128, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(L.paged_workspace_size(ctx.cfg, 1), dtype=torch.uint8, device="cuda")
+    for field, value, want in (("n_pages", 1 << 24, L.ERR_UNSUPPORTED), ("max_pages", (1 << 20) + 1, L.ERR_UNSUPPORTED),
+                               ("n_seqs", 8193, L.ERR_UNSUPPORTED), ("n_seqs", 0, L.ERR_SHAPE),
+                               ("page_tokens", 48, L.ERR_UNSUPPORTED), ("n_pages", 0, L.ERR_SHAPE)):
+        p = L.lowram_pages.from_buffer_copy(pages)
+        setattr(p, field, value)
+        r = ctypes.byref(p)
+        assert L.lowram_paged_attend(ctx.handle, r, q.data_ptr(), 1, q.data_ptr(), None, ws.data_ptr(),
+                                     ws.numel(), None) == want, field
+        assert L.lowram_paged_gather(ctx.handle, r, None, 1, q.data_ptr(), q.data_ptr(), None) == want, field
+        assert L.lowram_paged_append(ctx.handle, r, q.data_ptr(), q.data_ptr(), 1024, 1024, 1, None, 1,
+                                     None, 1, None) == want, field
+    p = L.lowram_pages.from_buffer_copy(pages)
+    p.table = p.table + 4
+    assert L.lowram_paged_attend(ctx.handle, ctypes.byref(p), q.data_ptr(), 1, q.data_ptr(), None,
+                                 ws.data_ptr(), ws.numel(), None) == L.ERR_ALIGN
+    p.table = None
+    assert L.lowram_paged_attend(ctx.handle, ctypes.byref(p), q.data_ptr(), 1, q.data_ptr(), None,
+                                 ws.data_ptr(), ws.numel(), None) == L.ERR_INVALID_ARG
+    ctx.close()
