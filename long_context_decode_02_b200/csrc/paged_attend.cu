@@ -520,6 +520,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
               if (__any_sync(0xffffffffu, nan)) {
                 if (!poison) {
                   poison = true;
+                  __syncwarp();   // the pair before has read its entries
                   for (int y = lane; y < D; y += 32) s_nan[warp][y] = 0x7fffffff;
                   __syncwarp();
                 }
@@ -529,6 +530,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
                   s_nan[warp][el] = min(s_nan[warp][el], tok0 + row);
                   bytes[e] = 0;
                 }
+                __syncwarp();   // another lane holds this element in the next row
               }
             }
           }
