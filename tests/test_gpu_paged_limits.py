@@ -1,7 +1,7 @@
 """Paged 8-bit cache at the ends of what include/lowram.h admits, against the plain 64-bit
-implementation: NaN values that several drafted tokens share.
+implementation: NaN values that several drafted tokens share, runs of millions of tokens.
 
-The tolerances are those of test_gpu_paged."""
+The tolerances are those of test_gpu_paged unless a test says otherwise."""
 import numpy as np
 import pytest
 import torch
@@ -51,4 +51,25 @@ def test_nan_value_in_one_element_of_consecutive_tokens(L, dtype, d, P):
     assert torch.equal(nan, want)
     ref = c.ref.attend(c.table, c.lens, f64(q), 2)
     check_attend(dtype, out[:, :1], lse[:, :1], tuple(x[:, :1] for x in ref))
+    ctx.close()
+
+
+def test_long_runs_of_a_warp(L):
+    """2^21 tokens of positive values for more (sequence, head)s than the GPU has warps, so a warp
+    sums a whole one: its 65536 steps add no bias. The sequences repeat one list of 4096 tokens,
+    whose exact result they share; lse is larger by the repetitions' logarithm."""
+    P, n, H, seqs = 64, 1 << 21, 8, 148
+    c = Case(L, [4096], P, H, 128, seed=71)
+    v = c.ref.code["v"] & 0x7f
+    c.ref.code["v"] = np.where(v == 0x7f, 0x38, v).astype(np.uint8)
+    q = torch.randn(1, 1, H, 128, generator=torch.Generator().manual_seed(1)).bfloat16()
+    out, lse, absv, zabs = c.ref.attend(c.table, c.lens, f64(q), 1)
+    c.table = np.tile(c.table[:, :4096 // P], (seqs, n // 4096))
+    c.lens = [n] * seqs
+    pages = c.device()
+    ctx = context(L, "bf16", H, 1, 128)
+    got, got_lse = attend(L, ctx, pages, q.repeat(seqs, 1, 1, 1).cuda(), 1)
+    want = (out, lse + np.log(n / 4096), absv, zabs)
+    for b in range(0, seqs, 21):
+        check_attend("bf16", got[b:b + 1], got_lse[b:b + 1], want, b)
     ctx.close()
