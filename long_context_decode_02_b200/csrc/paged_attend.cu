@@ -27,15 +27,21 @@
 // Numbers. A query row is scaled by a power of two to a largest magnitude in [2^12, 2^13) and
 // held in fp16: exact for bf16 rows (elements 2^-27 below the row's largest lose digits); fp32
 // rows take two columns, fp16(q) and fp16(q - fp16(q)), whose products add up to 2^-22. Scores,
-// the softmax's reference and sum and the output are fp32. A weight is rounded to fp16 (2^-11,
-// eight times finer than the bf16 output), for fp32 again in two columns (2^-22). The matrix
-// unit cuts its sums toward zero, by 2^-24 of the sum each time, so a step's product starts from
-// zero and is added to the output in fp32: carried on in the unit, 2^21 tokens of a run came out
-// 1.3 % too small.
-// Values carry their page's scale s_v = fr 2^ev inside the weight: the reference m of a row is
-// max(z + ev) over its tokens to within 2^6, so
-//   a = 2^(z + ev - m) <= 2^6,  weight = a fr 2^8 < 2^15,  sum += a 2^-ev,
-// and pages whose scales lie far apart cost each other no digits.
+// the softmax's reference and sum and the output are fp32. A weight a = 2^(z - m + 8) is rounded
+// to fp16 (2^-11, eight times finer than the bf16 output), for fp32 again in two columns (2^-22);
+// the row's reference m is the largest z so far to within 2^6, so a <= 2^14.
+// The matrix unit cuts its sums toward zero, by 2^-24 of the sum each time, so a step's product
+// starts from zero and is added to the output in fp32: carried on in the unit, 2^21 tokens of a
+// run came out 1.3 % too small.
+// Values' scales. A step's product is added times 2^(e - 40), e the largest exponent of the
+// step's v_scales; a weight carries what its page's scale is below that (>= 2^-8, or the next
+// form is taken), and the output is held in units of 2^32, where every sum of admitted scales
+// (2^-64 .. 2^120) is a normal number. So scales reach neither the softmax's sum nor one
+// another's digits. Where a unit's scale is more than 2^8 above the least of the run, its values
+// may matter at weights that fp16 cannot hold beside 1: the units of such a step each take their
+// own largest z as reference, and what that is above or below m goes into the fp32 factor.
+// (Every third page 2^20 smaller: batch 8 to 64K tokens 101.0 -> 102.3 us, fp32 40K 40.1 -> 46.5,
+// 5 drafted tokens 45.0 -> 54.1; near scales pay two integer operations a unit for the choice.)
 #include <cuda.h>
 
 #include "paged_common.cuh"
@@ -54,7 +60,11 @@ constexpr int kStages = 2;                // a warp's ring: 16 KB
 constexpr uint32_t kHalfBytes = 4096;     // K (or V) of a step
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kRingBytes = kStages * kStageBytes;
-constexpr float kWeightScale = 256.f;     // 2^8: weights in fp16 stay normal down to 2^-22
+constexpr int kWeightExp = 8;             // weights times 2^8: in fp16 normal down to 2^-22
+constexpr float kWeightScale = 1 << kWeightExp;
+constexpr int kOutExp = 32;               // the output's unit 2^32, with the weights' 2^8 taken out
+constexpr int kLeastExp = -64;            // of a scale
+constexpr int kNearExp = 8;               // spread of scales that weights may carry
 constexpr float kSlack = 6.f;             // log2 of what a weight may exceed its reference by
 constexpr int kCombineThreads = 256;
 
@@ -162,6 +172,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+// Over the lanes of a fragment's column.
+__device__ __forceinline__ float lanes_max(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
 __device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
 
 // Token (of 16) of fragment row x of S^T, and of row r that ldmatrix transposes for V. The two
@@ -187,7 +204,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
   constexpr int kC = D / 16, kOT = D / 16;          // 16-byte chunks of a row
   constexpr int NT = F32 ? RL : (RL + 1) / 2;       // column tiles
   extern __shared__ uint8_t smem_raw[];
-  __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, fr 2^8, ev, valid tokens
+  __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, v_scale, its exponent, tokens
   __shared__ int4 s_desc[kWarps][S];        // a stage's step: sequence, pair, first token, length
   __shared__ int2 s_part[kWarps][S];        // its partial; 1: begins one, 2: ends it
   __shared__ int s_nan[kWarps][D];          // first token with a NaN value that not all rows see
@@ -349,10 +366,9 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
     }
     if (first) {                     // behind the copies: the scales may still be on their way
       int ev = (int)((__float_as_uint(nsv) >> 23) & 255u) - 127;
-      ev = min(max(ev, -64), 120);
+      ev = nvalid > 0 ? min(max(ev, kLeastExp), 120) : kLeastExp - 1;   // below all: no unit
       s_meta[warp][(U * issued + lane) & (kMetaUnits - 1)] =
-          make_float4(nsk, nsv * __int_as_float((127 - ev) << 23) * kWeightScale,
-                      __int_as_float(ev), __int_as_float(nvalid));
+          make_float4(nsk, nsv, __int_as_float(ev), __int_as_float(nvalid));
       look_up();
     }
     --ccnt;
@@ -377,6 +393,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
   float cs[RL];                     // logit of a row in log2 units per unit of S
   int lim[RL];                      // tokens that the row sees
   float m[RL], l[RL], O[NT][kOT][4];
+  unsigned least_ev = 0;            // least exponent of a value's scale so far, from kLeastExp
   // the rows that this lane names to ldmatrix, in a step's K (a unit's) and V
   const int krow = s_token(lane & 15), vrow = v_token(lane & 15) + (lane & 16);   // two units' V
   bool good = true, poison = false;
@@ -396,6 +413,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
       if (part.y & 1) {   // a new (sequence, head, group): its queries
         const int b = ds.x, h = ds.y / p.rp.groups, len = ds.w;
         poison = false;
+        least_ev = 0xffffu;
         row0 = (ds.y - h * p.rp.groups) * p.rp.rows;
         vis = len - a.n_q + row0 / a.G + 1;
 #pragma unroll
@@ -539,83 +557,137 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         __syncwarp();
         fence_proxy_async_smem();   // before a copy fills the stage again
       }
-      // reference: the max of z + ev, moved only when a token exceeds it by 2^kSlack: few steps
-      // then pay for the reduction over the lanes and the output's rescaling
-      float ev[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) ev[u] = (float)__float_as_int(meta[u].z);
+      // reference: the max of z, moved only when a token exceeds it by 2^kSlack: few steps then
+      // pay for the reduction over the lanes and the output's rescaling
       float mn[RL];
       bool grow = false;
 #pragma unroll
       for (int x = 0; x < RL; ++x) {
-        mn[x] = fmaxf(z[0][x][0], z[0][x][1]) + ev[0];
+        mn[x] = fmaxf(z[0][x][0], z[0][x][1]);
 #pragma unroll
-        for (int u = 1; u < U; ++u) mn[x] = fmaxf(mn[x], fmaxf(z[u][x][0], z[u][x][1]) + ev[u]);
+        for (int u = 1; u < U; ++u) mn[x] = fmaxf(mn[x], fmaxf(z[u][x][0], z[u][x][1]));
         grow = grow || mn[x] > m[x] + kSlack;
       }
       if (__any_sync(0xffffffffu, grow)) {
-        float corr[RL];
+        float corr[RL];   // the factor's square root: tiny weights of huge values are no zeros
 #pragma unroll
         for (int x = 0; x < RL; ++x) {
-          float v = fmaxf(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          corr[x] = v > m[x] ? ex2_approx(m[x] - v) : 1.f;
+          const float v = lanes_max(mn[x]);
+          corr[x] = v > m[x] ? ex2_approx(0.5f * (m[x] - v)) : 1.f;
           m[x] = fmaxf(m[x], v);
-          l[x] *= corr[x];
+          l[x] *= corr[x] * corr[x];
         }
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int j = 0; j < kOT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) O[x][j][e] *= corr[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)];
+            for (int e = 0; e < 4; ++e) {
+              const float c = corr[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)];
+              O[x][j][e] = O[x][j][e] * c * c;
+            }
       }
       // weights, as B operands of O^T += V^T P^T
       uint32_t pf[U][NT][2];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const float back = __int_as_float((127 - __float_as_int(meta[u].z)) << 23);   // 2^-ev
-        const float sv = meta[u].y;
-        float wgt[RL][2];
-#pragma unroll
-        for (int x = 0; x < RL; ++x) {
-          const float off = m[x] == -INFINITY ? 0.f : ev[u] - m[x];
-          const float a0 = ex2_approx(z[u][x][0] + off), a1 = ex2_approx(z[u][x][1] + off);
-          l[x] = fmaf(a0 + a1, back, l[x]);
-          wgt[x][0] = a0 * sv;
-          wgt[x][1] = a1 * sv;
-        }
+      auto operand = [&](const float (&wgt)[RL][2], uint32_t (&f)[NT][2]) {
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float hi = wgt[F32 || RL == 1 ? x : 2 * x][k];
             const float lo = F32 ? hi - round_f16(hi) : RL == 1 ? 0.f : wgt[RL == 1 ? 0 : 2 * x + 1][k];
-            pf[u][x][k] = movmatrix_trans(pack_f16x2(hi, lo));
+            f[x][k] = movmatrix_trans(pack_f16x2(hi, lo));
           }
+      };
+      int top = kLeastExp - 1;   // the step's largest exponent of a value's scale
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int ev = __float_as_int(meta[u].z);
+        top = max(top, ev);
+        least_ev = min(least_ev, (unsigned)(ev - kLeastExp));   // no unit: above all
       }
-      // O^T += V^T P^T
+      if (top - kLeastExp <= (int)least_ev + kNearExp) {
+        const float down = pow2f(-top);
 #pragma unroll
-      for (int j = 0; j < kOT; ++j) {
-        float o[NT][4];
+        for (int u = 0; u < U; ++u) {
+          const float sv = meta[u].y * down;
+          float wgt[RL][2];
 #pragma unroll
-        for (int u = 0; u < U; u += 2) {
-          uint32_t f[4], f0[4], f1[4];
-          ldmatrix_b8_trans(vb + chunk_offset<D>(u * kUnit + vrow, j), f);   // elements 16 j ..
-          widen(f[0], f[1], f0);
-          widen(f[2], f[3], f1);
+          for (int x = 0; x < RL; ++x) {
+            const float off = m[x] == -INFINITY ? 0.f : kWeightExp - m[x];
+            const float a0 = ex2_approx(z[u][x][0] + off), a1 = ex2_approx(z[u][x][1] + off);
+            l[x] += a0 + a1;
+            wgt[x][0] = a0 * sv;
+            wgt[x][1] = a1 * sv;
+          }
+          operand(wgt, pf[u]);
+        }
+        // O^T += V^T P^T
+        const float unit = pow2f(top - kWeightExp - kOutExp);
 #pragma unroll
-          for (int x = 0; x < NT; ++x) {
-            if (u == 0) mma_f16_first(o[x], f0, pf[u][x][0], pf[u][x][1]);
-            else mma_f16(o[x], f0, pf[u][x][0], pf[u][x][1]);
-            mma_f16(o[x], f1, pf[u + 1][x][0], pf[u + 1][x][1]);
+        for (int j = 0; j < kOT; ++j) {
+          float o[NT][4];
+#pragma unroll
+          for (int u = 0; u < U; u += 2) {
+            uint32_t f[4], f0[4], f1[4];
+            ldmatrix_b8_trans(vb + chunk_offset<D>(u * kUnit + vrow, j), f);   // elements 16 j ..
+            widen(f[0], f[1], f0);
+            widen(f[2], f[3], f1);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              if (u == 0) mma_f16_first(o[x], f0, pf[u][x][0], pf[u][x][1]);
+              else mma_f16(o[x], f0, pf[u][x][0], pf[u][x][1]);
+              mma_f16(o[x], f1, pf[u + 1][x][0], pf[u + 1][x][1]);
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) O[x][j][e] = fmaf(o[x][e], unit, O[x][j][e]);
+        }
+      } else {
+        // scales far apart: a unit at a time, from its own largest z. Four units are not unrolled
+        // (unit 0 of z, the others moved up): they would not fit the registers.
+        constexpr bool kRoll = U > 2;
+#pragma unroll (kRoll ? 1 : U)
+        for (int u = 0; u < U; ++u) {
+          const int zu = kRoll ? 0 : u;
+          const int ev = __float_as_int(meta[u].z);
+          const float sv = meta[u].y * pow2f(-ev);
+          float wgt[RL][2], unit[RL];
+#pragma unroll
+          for (int x = 0; x < RL; ++x) {
+            const float r = lanes_max(fmaxf(z[zu][x][0], z[zu][x][1]));
+            const bool some = r != -INFINITY;
+            const float off = some ? kWeightExp - r : 0.f;
+            const float back = some ? exp2f(r - m[x]) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              wgt[x][k] = ex2_approx(z[zu][x][k] + off);
+              l[x] = fmaf(wgt[x][k], back, l[x]);
+              if (kRoll) {
+#pragma unroll
+                for (int w = 1; w < U; ++w) z[w - 1][x][k] = z[w][x][k];
+              }
+            }
+            unit[x] = some ? exp2f(r - m[x] + (float)(ev - kWeightExp - kOutExp)) * sv : 0.f;
+          }
+          operand(wgt, pf[zu]);
+#pragma unroll
+          for (int j = 0; j < kOT; ++j) {
+            uint32_t f[4], fu[4];
+            ldmatrix_b8_trans(vb + chunk_offset<D>((u & ~1) * kUnit + vrow, j), f);
+            widen(u & 1 ? f[2] : f[0], u & 1 ? f[3] : f[1], fu);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) {
+              float o[4];
+              mma_f16_first(o, fu, pf[zu][x][0], pf[zu][x][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                O[x][j][e] = fmaf(o[e], unit[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)], O[x][j][e]);
+            }
           }
         }
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) O[x][j][e] += o[x][e];
       }
       // end of the pair, or of the run: its partial
       if (part.y & 2) {
@@ -658,13 +730,28 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
   }
 }
 
+// Weight 2^(m - top) of a partial with reference m: 1 where it saw nothing and holds zeros (a NaN
+// sum must stay one).
+__device__ __forceinline__ float weight_of(float m, float top) {
+  return m == -INFINITY ? 1.f : ex2_approx(m - top);
+}
+// Its root, to be applied twice: a weight that is no fp32 number may be that of huge values.
+__device__ __forceinline__ float root_weight(float m, float top) {
+  return weight_of(0.5f * m, 0.5f * top);
+}
+__device__ __forceinline__ bool is_tiny(float m, float top) {
+  return m != -INFINITY && m - top < -126.f;
+}
+
 // One CTA a query row: out = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s over the partials
 // of its pair. The warps take every eighth partial, four of them in flight together (one after
 // another, the 129 partials of a 4K sequence took 6 us). Where the partials lie follows from the
 // lengths; up to 32 sequences it is worked out while the first kernel runs. A compressed prefix
-// joins as one more partial.
+// joins as one more partial. Five CTAs an SM, so 48 registers: one then fits beside a CTA of the
+// first kernel (up to 208, as one query in bf16 has) and is set up early (with 66: one sequence of
+// 600 tokens 7.4 us instead of 6.7).
 template <typename T, int D>
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kCombineThreads, 5) paged_combine_kernel(const AttendParams p) {
   constexpr int E = D / 32, kW = kCombineThreads / 32, kStep = Tile<D>::kStep;
   const PagedArgs& a = p.a;
   const lowram_pages& pg = a.pg;
@@ -700,6 +787,7 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  bool tiny = false;
   constexpr int kU = 4;   // partials of a warp in flight together
   for (int s0 = warp; s0 < count; s0 += kU * kW) {
     float2 x[kU];
@@ -723,18 +811,32 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) mn = fmaxf(mn, x[u].x);
-    // what saw nothing holds zeros; a NaN sum must stay one
-    const float c = m == -INFINITY ? 1.f : ex2_approx(m - mn);
+    tiny = tiny || is_tiny(m, mn);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) tiny = tiny || is_tiny(x[u].x, mn);
+    const float c = weight_of(m, mn);
     m = mn;
     l *= c;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= c;
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const float w = x[u].x == -INFINITY ? 1.f : ex2_approx(x[u].x - mn);
+      const float w = weight_of(x[u].x, mn);
       l = fmaf(w, x[u].y, l);
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = fmaf(w, o[u][e], acc[e]);
+    }
+  }
+  if (tiny) {   // (rare) once more, from the largest reference and in two steps
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int s = warp; s < count; s += kW) {
+      const float2 x = ml[(size_t)s * p.rp.rows];
+      const float w = root_weight(x.x, m);
+      l = fmaf(w * w, x.y, l);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(w, po[s * so + e] * w, acc[e]);
     }
   }
   __shared__ float s_m[kW], s_l[kW], s_o[kW][D];
@@ -748,29 +850,30 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const At
   float M = -INFINITY, L = 0.f, w[kW];
 #pragma unroll
   for (int x = 0; x < kW; ++x) M = fmaxf(M, s_m[x]);
-  float pm = 0.f, pl = 0.f;   // a compressed prefix's softmax, max in log2 units
+  float pw = 0.f, pl = 0.f;   // a compressed prefix's softmax, max in log2 units
   if (a.pre_ml) {
-    pm = a.pre_ml[2 * row] * 1.4426950408889634f;
-    pl = a.pre_ml[2 * row + 1];
+    const float pm = a.pre_ml[2 * row] * 1.4426950408889634f;
     M = fmaxf(M, pm);
-    pl *= ex2_approx(pm - M);
-    L = pl;
+    pw = root_weight(pm, M);
+    pl = a.pre_ml[2 * row + 1] * kWeightScale;
+    L = pl * pw * pw;
   }
 #pragma unroll
   for (int x = 0; x < kW; ++x) {
-    w[x] = s_m[x] == -INFINITY ? 1.f : ex2_approx(s_m[x] - M);
-    L = fmaf(w[x], s_l[x], L);
+    w[x] = root_weight(s_m[x], M);
+    L = fmaf(w[x] * w[x], s_l[x], L);
   }
-  const float inv = L == 0.f ? 0.f : 1.f / (L * kWeightScale);
+  const float inv = L == 0.f ? 0.f : pow2f(kWeightExp + kOutExp) / L;
   if (threadIdx.x < D) {
     float o = 0.f;
 #pragma unroll
-    for (int x = 0; x < kW; ++x) o = fmaf(w[x], s_o[x][threadIdx.x], o);
-    if (a.pre_ml) o = fmaf(a.pre_out[row * D + threadIdx.x], pl * kWeightScale, o);
+    for (int x = 0; x < kW; ++x) o = fmaf(w[x], s_o[x][threadIdx.x] * w[x], o);
+    if (a.pre_ml)
+      o = fmaf(pw, a.pre_out[row * D + threadIdx.x] * pow2f(-kWeightExp - kOutExp) * pl * pw, o);
     ((T*)a.out)[row * D + threadIdx.x] = from_f<T>(o * inv);
   }
   if (a.lse && threadIdx.x == 0)
-    a.lse[row] = L == 0.f ? -INFINITY : fmaf(M, 0.69314718055994531f, logf(L));
+    a.lse[row] = L == 0.f ? -INFINITY : fmaf(M, 0.69314718055994531f, logf(L * (1.f / kWeightScale)));
 }
 
 template <typename T, int D, int RL, bool F32>

@@ -1,12 +1,17 @@
 """Paged 8-bit cache at the ends of what include/lowram.h admits, against the plain 64-bit
-implementation: NaN values that several drafted tokens share, runs of millions of tokens.
+implementation: NaN values that several drafted tokens share, runs of millions of tokens,
+value scales anywhere in 2^-64 .. 2^120.
 
 The tolerances are those of test_gpu_paged unless a test says otherwise."""
 import numpy as np
 import pytest
 import torch
 
+from long_context_decode_02_b200 import synth
+from tests import paged_reference as R
+from tests.test_gpu_decode import prepared
 from tests.test_gpu_paged import DT, Case, check_attend, context, f64
+from tests.test_gpu_paged_decode import BF16, F32, check_step, new_pages, suffix_values
 
 pytestmark = pytest.mark.gpu
 
@@ -72,4 +77,116 @@ def test_long_runs_of_a_warp(L):
     want = (out, lse + np.log(n / 4096), absv, zabs)
     for b in range(0, seqs, 21):
         check_attend("bf16", got[b:b + 1], got_lse[b:b + 1], want, b)
+    ctx.close()
+
+
+def scaled(L, lens, P, H, d, seed, lo, hi, one_element=False):
+    """A case whose pages have value scales 2^lo and 2^hi in turn (two of a kind now and then),
+    the large ones' codes small enough to stay finite. one_element: a large page has values in
+    element 3 only, so that the other elements show what the small pages keep of their digits."""
+    c = Case(L, lens, P, H, d, seed=seed)
+    g = np.random.default_rng(seed)
+    for row, n in zip(c.table, lens):
+        for i in range(-(-n // P)):
+            big = bool(i & 1) != (g.random() < 0.25)
+            c.ref.scale["v"][row[i]] = 2.0 ** (hi if big else lo)
+            if big:
+                c.ref.code["v"][row[i]] = R.encode(np.clip(R.decode(c.ref.code["v"][row[i]]), -240, 240))
+                if one_element:
+                    c.ref.code["v"][row[i], ..., :3] = 0
+                    c.ref.code["v"][row[i], ..., 4:] = 0
+    return c
+
+
+SCALES = [(-64, 62), (-64, 63), (-64, 84), (-64, 120), (-8, 120), (-20, 14), (-8, 0), (-7, 2)]
+
+
+@pytest.mark.parametrize("one_element", [False, True])
+@pytest.mark.parametrize("dtype,G,d,P,nq,lens", [
+    ("bf16", 4, 128, 16, 1, [77, 200]),
+    ("bf16", 8, 128, 64, 1, [300]),
+    ("bf16", 8, 128, 16, 3, [50, 2]),
+    ("bf16", 4, 64, 32, 4, [150]),
+    ("bf16", 1, 64, 16, 1, [90]),
+    ("f32", 4, 64, 16, 1, [100, 31]),
+    ("f32", 4, 128, 32, 2, [150]),
+    ("f32", 2, 64, 64, 1, [400]),
+])
+def test_value_scales_far_apart(L, dtype, G, d, P, nq, lens, one_element):
+    """Tokens of about the same weight in pages whose value scales lie anywhere in the admitted
+    range: none leaves the softmax's sum, and each element keeps its digits."""
+    ctx = context(L, dtype, 2, G, d)
+    q = torch.randn(len(lens), nq, 2 * G, d, generator=torch.Generator().manual_seed(d + nq)) / 8
+    q = q.to(DT[dtype]).cuda()
+    for i, (lo, hi) in enumerate(SCALES):
+        c = scaled(L, lens, P, 2, d, 80 + i, lo, hi, one_element)
+        out, lse = attend(L, ctx, c.device(), q, G)
+        check_attend(dtype, out, lse, c.ref.attend(c.table, c.lens, f64(q), G), (lo, hi))
+    ctx.close()
+
+
+@pytest.mark.parametrize("dtype,d,P", [("bf16", 128, 64), ("bf16", 128, 16), ("f32", 64, 32)])
+def test_value_scales_far_apart_over_runs(L, dtype, d, P):
+    """The same where a warp's run has several steps and a row many partials."""
+    H = 4
+    ctx = context(L, dtype, H, 1, d)
+    q = torch.randn(2, 1, H, d, generator=torch.Generator().manual_seed(7)).to(DT[dtype]).cuda() / 8
+    for lo, hi in ((-64, 63), (-64, 120), (-8, 30)):
+        c = scaled(L, [29000, 700], P, H, d, 90, lo, hi, one_element=hi == 30)
+        out, lse = attend(L, ctx, c.device(), q, 1)
+        check_attend(dtype, out, lse, c.ref.attend(c.table, c.lens, f64(q), 1), (lo, hi))
+    ctx.close()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("P,H,n", [(16, 1, 64), (64, 1, 2530), (32, 4, 17000)])
+def test_tiny_weights_of_huge_values(L, dtype, P, H, n):
+    """Logits that give the large pages weights far below what fp16, or one fp32 exponential,
+    holds beside 1, though their values make up the output: within a step, over the partials of a
+    row, and over a warp's run of steps."""
+    d = 64
+    for lo, hi, drop in ((-8, 40, 25), (-64, 60, 80), (-64, 119, 112), (-64, 119, 160)):
+        for first in (0, 1):
+            c = Case(L, [n], P, H, d, seed=99)
+            c.ref.code["k"][:] = 0
+            c.ref.scale["k"][:] = 1.0
+            for i, page in enumerate(c.table[0, :-(-n // P)]):
+                big = i % 2 == first
+                c.ref.scale["v"][page] = 2.0 ** (hi if big else lo)
+                if big:      # z = q k / 8 with q = 4 ln 2: a weight of 2^-drop
+                    c.ref.code["k"][page, ..., 0] = R.encode(np.array(-2.0 * drop))
+                c.ref.code["v"][page] = R.encode(np.clip(R.decode(c.ref.code["v"][page]), -240, 240))
+            # the codes behind the length are NaN still
+            if n % P:
+                c.ref.code["v"][c.table[0, n // P], :, n % P:, 0] = 0x7f
+            q = torch.zeros(1, 1, 2 * H, d)
+            q[..., 0] = 4 * np.log(2.0)
+            q = q.to(DT[dtype]).cuda()
+            ctx = context(L, dtype, H, 2, d)
+            out, lse = attend(L, ctx, c.device(), q, 2)
+            check_attend(dtype, out, lse, c.ref.attend(c.table, c.lens, f64(q), 2), (lo, hi, drop, first))
+            ctx.close()
+
+
+@pytest.mark.parametrize("sh,exp", [(BF16, 119), (BF16, -60), (F32, 110)])
+def test_prefix_beside_far_scales(L, cuda_device, sh, exp):
+    """A compressed prefix and a suffix whose values are 2^exp times as large: the softmax spans
+    both."""
+    dev, P, lens = cuda_device, 16, [3, 40][:sh.batch - 1] + [200]
+    t, t_dev, cdev, co, _ = prepared(sh, 0, dev)
+    cfg = L.make_config(sh)
+    ctx = L.Context(cfg, dev.index or 0)
+    params = L.layer_params(*(t_dev[n] for n in ("basis", "w1", "b1", "w2", "b2")))
+    pages, pt, table, dlens = new_pages(L, sh, P, max(lens) + 1, dev)
+    n = sum(lens)
+    g = torch.Generator().manual_seed(97)
+    k, v = (torch.randn(n, sh.n_kv_heads, sh.head_dim, generator=g) for _ in "kv")
+    v[lens[0]:] *= 2.0 ** exp          # sequence 0 keeps values of the prefix's size
+    k, v = k.to(sh.torch_dtype).to(dev), v.to(sh.torch_dtype).to(dev)
+    dlens.copy_(torch.tensor(lens, dtype=torch.int32))
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=dev)
+    L.paged_append(ctx, pages, k, v, cu_new=cu, pos_base=torch.full_like(dlens, sh.n_tokens))
+    ws = torch.empty(L.decode_paged_workspace_size(cfg), dtype=torch.uint8, device=dev).fill_(255)
+    sk, sv = (suffix_values(pt, table, lens, x) for x in "kv")
+    check_step(L, sh, ctx, cdev, t, co, params, synth.queries(sh, 0, 0), pages, sk, sv, ws, dev)
     ctx.close()
