@@ -28,8 +28,10 @@
 // held in fp16: exact for bf16 rows (elements 2^-27 below the row's largest lose digits); fp32
 // rows take two columns, fp16(q) and fp16(q - fp16(q)), whose products add up to 2^-22. Scores,
 // the softmax's reference and sum and the output are fp32. A weight a = 2^(z - m + 8) is rounded
-// to fp16 (2^-11, eight times finer than the bf16 output), for fp32 again in two columns (2^-22);
-// the row's reference m is the largest z so far to within 2^6, so a <= 2^14.
+// to fp16: in two columns where they are free (fp32, and up to 4 bf16 rows: 2^-22), in one for
+// more bf16 rows (2^-11, eight times finer than the output; a second column would double their
+// products, and they are bound by instructions). The row's reference m is the largest z so far to
+// within 2^6, so a <= 2^14.
 // The matrix unit cuts its sums toward zero, by 2^-24 of the sum each time, so a step's product
 // starts from zero and is added to the output in fp32: carried on in the unit, 2^21 tokens of a
 // run came out 1.3 % too small.
@@ -194,15 +196,19 @@ template <int D> __device__ __forceinline__ uint32_t chunk_offset(int row, int c
 }
 
 // RL: query rows of a lane, 4 RL of a group. Columns 2 t, 2 t + 1 of a tile are, in fp32, the
-// high and low parts of row 4 x + t (tile x); in bf16 row t and nothing (RL = 1), or rows
-// 8 x + 2 t, 8 x + 2 t + 1 (tile x).
+// high and low parts of row 4 x + t (tile x); in bf16 row t, its weights in two parts and its
+// query in one (RL = 1), or rows 8 x + 2 t, 8 x + 2 t + 1 (tile x).
+//
+// 208 registers where RL = 1: a CTA of the merge then fits beside one of this kernel and is set up
+// early (with 211: one 4K sequence 15.0 us instead of 9.7).
 template <typename T, int D, int RL, bool F32>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __maxnreg__(RL == 1 ? 208 : 255)
 paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps maps) {
   using TL = Tile<D>;
   constexpr int S = kStages, U = TL::kUnits, kStep = TL::kStep;
   constexpr int kC = D / 16, kOT = D / 16;          // 16-byte chunks of a row
   constexpr int NT = F32 ? RL : (RL + 1) / 2;       // column tiles
+  constexpr bool kParts = F32 || RL == 1;           // weights in two columns
   extern __shared__ uint8_t smem_raw[];
   __shared__ float4 s_meta[kWarps][kMetaUnits];   // a unit: k_scale, v_scale, its exponent, tokens
   __shared__ int4 s_desc[kWarps][S];        // a stage's step: sequence, pair, first token, length
@@ -583,7 +589,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
           for (int j = 0; j < kOT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float c = corr[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)];
+              const float c = corr[kParts ? x : 2 * x + (e & 1)];
               O[x][j][e] = O[x][j][e] * c * c;
             }
       }
@@ -594,8 +600,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float hi = wgt[F32 || RL == 1 ? x : 2 * x][k];
-            const float lo = F32 ? hi - round_f16(hi) : RL == 1 ? 0.f : wgt[RL == 1 ? 0 : 2 * x + 1][k];
+            const float hi = wgt[kParts ? x : 2 * x][k];
+            const float lo = kParts ? hi - round_f16(hi) : wgt[kParts ? 0 : 2 * x + 1][k];
             f[x][k] = movmatrix_trans(pack_f16x2(hi, lo));
           }
       };
@@ -684,7 +690,7 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
               mma_f16_first(o, fu, pf[zu][x][0], pf[zu][x][1]);
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                O[x][j][e] = fmaf(o[e], unit[F32 ? x : RL == 1 ? 0 : 2 * x + (e & 1)], O[x][j][e]);
+                O[x][j][e] = fmaf(o[e], unit[kParts ? x : 2 * x + (e & 1)], O[x][j][e]);
             }
           }
         }
@@ -707,8 +713,8 @@ paged_attend_kernel(const AttendParams p, const __grid_constant__ AttendMaps map
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int el = 16 * j + g + 8 * k;
-                float o = F32 ? O[F32 ? x : 0][j][2 * k] + O[F32 ? x : 0][j][2 * k + 1]
-                              : O[x >> 1][j][2 * k + (x & 1)];
+                float o = kParts ? O[kParts ? x : 0][j][2 * k] + O[kParts ? x : 0][j][2 * k + 1]
+                                 : O[x >> 1][j][2 * k + (x & 1)];
                 if (poison && s_nan[warp][el] < lim[x]) o = __int_as_float(0x7fffffff);
                 po[(size_t)r * D + el] = o;
               }
@@ -748,8 +754,7 @@ __device__ __forceinline__ bool is_tiny(float m, float top) {
 // another, the 129 partials of a 4K sequence took 6 us). Where the partials lie follows from the
 // lengths; up to 32 sequences it is worked out while the first kernel runs. A compressed prefix
 // joins as one more partial. Five CTAs an SM, so 48 registers: one then fits beside a CTA of the
-// first kernel (up to 208, as one query in bf16 has) and is set up early (with 66: one sequence of
-// 600 tokens 7.4 us instead of 6.7).
+// first kernel (with 66: one sequence of 600 tokens 7.4 us instead of 6.7).
 template <typename T, int D>
 __global__ void __launch_bounds__(kCombineThreads, 5) paged_combine_kernel(const AttendParams p) {
   constexpr int E = D / 32, kW = kCombineThreads / 32, kStep = Tile<D>::kStep;

@@ -1,6 +1,6 @@
 """Paged 8-bit cache at the ends of what include/lowram.h admits, against the plain 64-bit
 implementation: NaN values that several drafted tokens share, runs of millions of tokens,
-value scales anywhere in 2^-64 .. 2^120.
+value scales anywhere in 2^-64 .. 2^120, outputs that cancel.
 
 The tolerances are those of test_gpu_paged unless a test says otherwise."""
 import numpy as np
@@ -189,4 +189,37 @@ def test_prefix_beside_far_scales(L, cuda_device, sh, exp):
     ws = torch.empty(L.decode_paged_workspace_size(cfg), dtype=torch.uint8, device=dev).fill_(255)
     sk, sv = (suffix_values(pt, table, lens, x) for x in "kv")
     check_step(L, sh, ctx, cdev, t, co, params, synth.queries(sh, 0, 0), pages, sk, sv, ws, dev)
+    ctx.close()
+
+
+@pytest.mark.parametrize("G,nq,d", [(4, 1, 128), (1, 1, 64), (2, 2, 64), (1, 4, 128)])
+def test_weights_of_up_to_four_bf16_rows(L, G, nq, d):
+    """Up to four query rows of a head hold their weights in two fp16 parts, 2^-21 together, as
+    fp32 contexts do. It shows where an output cancels: two tokens of weights a and b with values
+    near b and -a, so that its own rounding is small beside sum p |v|. Keys and queries have one
+    element, which keeps the logits' share of the bound at (d + 8) 2^-22 |z|."""
+    seqs, P = 24, 16
+    c = Case(L, [nq + 1] * seqs, P, 1, d, seed=72)
+    g = np.random.default_rng(73)
+    q = torch.zeros(seqs, nq, G, d)
+    q[..., 0] = 1.0
+    k, v, r = c.ref.code["k"], c.ref.code["v"], c.table[:, 0]
+    c.ref.scale["k"][:] = 2.0 ** -3
+    k[r, 0, :nq + 1] = 0
+    v[r, 0, :nq + 1] = 0
+    # the last query's weights: token nq at e^z of the others, token 0 holds the other value
+    k[r, 0, nq, 0] = R.encode(-(8.0 + 4.0 * np.arange(seqs)))
+    z = R.decode(k[r, 0, nq, 0]) / 8 / d ** 0.5
+    first = np.exp2(g.uniform(2, 5.5, size=(seqs, d))) * g.choice([-1, 1], size=(seqs, d))
+    v[r, 0, 0] = R.encode(first)
+    v[r, 0, nq] = R.encode(-R.decode(v[r, 0, 0]) * np.exp(-z)[:, None])
+    pages = c.device()
+    ctx = context(L, "bf16", 1, G, d)
+    qd = q.bfloat16().cuda()
+    out, lse = attend(L, ctx, pages, qd, G)
+    want, _, absv, zabs = c.ref.attend(c.table, c.lens, f64(qd), G)
+    ez = (d + 8) * 2.0 ** -22 * zabs + 2.0 ** -20
+    tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -21 + 2 * ez[..., None]) * absv
+    over = np.abs(f64(out) - want) - tol
+    assert over.max() <= 0, (over.max(), (over / absv.clip(1e-30)).max())
     ctx.close()
