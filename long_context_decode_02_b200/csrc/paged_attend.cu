@@ -765,7 +765,6 @@ __global__ void __launch_bounds__(kCombineThreads, 5) paged_combine_kernel(const
   const int grp = r / p.rp.rows, rg = r % p.rp.rows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pairs = a.H * p.rp.groups, pair = h * p.rp.groups + grp;
-  grid_launch_dependents();
   long long total, before;
   int ns;
   if (pg.n_seqs <= 32) {
@@ -789,6 +788,7 @@ __global__ void __launch_bounds__(kCombineThreads, 5) paged_combine_kernel(const
   const size_t so = (size_t)p.rp.rows * D;
   const size_t row = ((size_t)b * a.n_q + j) * a.Hq + hq;
   grid_dependency_wait();
+  grid_launch_dependents();
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
