@@ -451,7 +451,6 @@ def paged_cache(k_code, v_code, k_scale, v_scale, table, lens) -> lowram_pages:
                      _ptr(lens), table.shape[0], table.shape[1], k_code.shape[0],
                      k_code.shape[2])
     p._refs = (k_code, v_code, k_scale, v_scale, table, lens)
-    p._ref = ctypes.byref(p)
     p._heads = (k_code.shape[1], k_code.shape[3])
     p._device = k_code.get_device()
     # what the calls below look up every time
@@ -524,7 +523,7 @@ def paged_append(ctx: Context, pages: lowram_pages, k_new, v_new, cu_new=None, m
             if n > 1:
                 ks, vs = a[0], b[0]
     n_seqs = pages.n_seqs
-    st = lowram_paged_append(ctx._h, pages._ref, k_new.data_ptr(), v_new.data_ptr(), ks, vs, n,
+    st = lowram_paged_append(ctx._h, pages, k_new.data_ptr(), v_new.data_ptr(), ks, vs, n,
                              _int32(pages, cu_new, n_seqs + 1, "cu_new"),
                              n if max_new is None else max_new,
                              _int32(pages, pos_base, n_seqs, "pos_base"), 1 if rotate else 0,
@@ -555,7 +554,7 @@ def paged_attend(ctx: Context, pages: lowram_pages, q, out, workspace, lse=None,
         raise ValueError(f"q and out must be {dt}")
     if lse is not None and (lse.dtype != pages._float32 or lse.shape != shape[:-1]):
         raise ValueError(f"lse must be fp32 of shape {tuple(shape[:-1])}")
-    st = lowram_paged_attend(ctx._h, pages._ref, q.data_ptr(), shape[1] if len(shape) == 4 else 1,
+    st = lowram_paged_attend(ctx._h, pages, q.data_ptr(), shape[1] if len(shape) == 4 else 1,
                              out.data_ptr(), None if lse is None else lse.data_ptr(),
                              workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                              _paged_stream(ctx, pages, stream))
@@ -575,7 +574,7 @@ def paged_gather(ctx: Context, pages: lowram_pages, k_out, v_out, start=None,
     dt = pages._dtype[ctx.cfg.dtype]
     if k_out.dtype != dt or v_out.dtype != dt:
         raise ValueError(f"k_out and v_out must be {dt}")
-    st = lowram_paged_gather(ctx._h, pages._ref, _int32(pages, start, pages.n_seqs, "start"), shape[1],
+    st = lowram_paged_gather(ctx._h, pages, _int32(pages, start, pages.n_seqs, "start"), shape[1],
                              k_out.data_ptr(), v_out.data_ptr(), _paged_stream(ctx, pages, stream))
     if st != OK:
         raise LowRAMError(st, "lowram_paged_gather")
@@ -599,6 +598,6 @@ def decode_step_paged(ctx: Context, cache: dict, params: lowram_layer_params, q,
         raise ValueError(f"q and out must be {dt} of shape {shape}")
     cs = cache_struct(**cache)
     check(lowram_decode_step_paged(ctx.handle, ctypes.byref(cs), ctypes.byref(params), _ptr(q),
-                                   pages._ref, _ptr(out), _ptr(sel_out), _ptr(workspace),
+                                   pages, _ptr(out), _ptr(sel_out), _ptr(workspace),
                                    workspace.numel() * workspace.element_size(),
                                    _paged_stream(ctx, pages, stream)), "lowram_decode_step_paged")
