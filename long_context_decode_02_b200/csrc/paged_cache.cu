@@ -245,7 +245,7 @@ paged_append_kernel(const PagedArgs a) {
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs a) {
   constexpr int E = 16 / sizeof(T), kLanes = D / E;   // codes of a store, lanes of a row
-  constexpr int kRows = 32 / kLanes > 0 ? 32 / kLanes : 1, kParts = kLanes > 32 ? kLanes / 32 : 1;
+  constexpr int kRows = 32 / kLanes;                  // rows of a warp's store
   const lowram_pages& pg = a.pg;
   const int P = pg.page_tokens, b = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -272,26 +272,26 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs 
   const uint8_t* src = codes + ph * (size_t)P * D;
   const int r0 = lane / kLanes, el = (lane % kLanes) * E;
   constexpr int kU = 8;
-  for (int r = lo; r < hi; r += kU * kRows / kParts) {
+  for (int r = lo; r < hi; r += kU * kRows) {
     uint32_t w[kU][E / 4];
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int row = r + (k / kParts) * kRows + r0, e0 = el + (k % kParts) * 32 * E;
+      const int row = r + k * kRows + r0;
 #pragma unroll
       for (int e = 0; e < E / 4; ++e) w[k][e] = 0;
       if (row < held) {
         if constexpr (E == 8) {
-          const uint2 y = *reinterpret_cast<const uint2*>(src + row * D + e0);
+          const uint2 y = *reinterpret_cast<const uint2*>(src + row * D + el);
           w[k][0] = y.x;
           w[k][1] = y.y;
         } else {
-          w[k][0] = *reinterpret_cast<const uint32_t*>(src + row * D + e0);
+          w[k][0] = *reinterpret_cast<const uint32_t*>(src + row * D + el);
         }
       }
     }
 #pragma unroll
     for (int k = 0; k < kU; ++k) {
-      const int row = r + (k / kParts) * kRows + r0, e0 = el + (k % kParts) * 32 * E;
+      const int row = r + k * kRows + r0;
       if (row >= hi) continue;
       float x[E];
       alignas(16) T y[E];
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(const PagedArgs 
       for (int e = 0; e < E / 4; ++e) e4m3x4_to_float(w[k][e], x + 4 * e);
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = from_f<T>(x[e] * s);
-      *reinterpret_cast<uint4*>(out + ((size_t)(t0 + row - start) * a.H + h) * D + e0) =
+      *reinterpret_cast<uint4*>(out + ((size_t)(t0 + row - start) * a.H + h) * D + el) =
           *reinterpret_cast<const uint4*>(y);
     }
   }
