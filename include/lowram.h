@@ -292,7 +292,8 @@ lowram_status lowram_append(lowram_ctx* dst_ctx, const lowram_cache* dst,
  *                    bits, no infinities, 0x7f / 0xff = NaN);
  *   k_scale, v_scale [n_pages][H_kv] fp32, positive: value = code * scale. lowram_paged_append
  *                    writes powers of two 2^e, -64 <= e <= 120; scales written elsewhere must
- *                    lie in that range;
+ *                    lie in that range (not checked; a NaN value scale may reach every
+ *                    query of its sequence, those before its page too);
  *   table            [n_seqs][max_pages] int32: token t of sequence b is row t % page_tokens of
  *                    page table[b][t / page_tokens]. Entries past a sequence's last page are
  *                    never read;

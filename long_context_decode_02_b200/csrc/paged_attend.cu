@@ -1,8 +1,9 @@
 // Attention over the paged 8-bit cache for the last n_q tokens of every sequence:
 //   z_t = (q . k_code_t) k_scale / sqrt(d),  out = sum_t softmax(z)_t v_code_t v_scale.
 //
-// Bound by bytes: each code is read once (2 sum(len) H d bytes), for 4 G n_q operations a pair
-// of codes. The work is cut into steps of 8 KB (32 tokens, 64 for d = 64) of one (sequence, KV
+// Bound by bytes: each group of 16 query rows of a head (8 in fp32) reads each code once
+// (2 sum(len) H d bytes a group), for 4 G n_q operations a pair of codes; with several groups,
+// and in fp32, by instructions. The work is cut into steps of 8 KB (32 tokens, 64 for d = 64) of one (sequence, KV
 // head, group of query rows), all in one list, an equal run of them for every warp of the GPU, so
 // ragged batches and single long sequences fill it alike. A warp streams its run alone: it issues
 // TMA boxes into its own ring of stages, holds the queries as matrix fragments in registers, and
@@ -11,8 +12,8 @@
 //
 // Two stages a warp, not three: with 192 KB of an SM always asked for, four groups of ten SMs get
 // a tenth less of the bandwidth than the others and end that much later (batch 8 at 128K tokens:
-// SMs end at 280 .. 350 us); with 128 KB all get the same (300 .. 319 us; the call 354 -> 326 us,
-// now 320, 6.7 TB/s; over caches that find nothing in the L2 328 .. 341).
+// SMs end at 280 .. 350 us); with 128 KB all get the same (300 .. 319 us; the call 354 -> 326 us;
+// now, over caches that find nothing in the L2, 318 .. 345 by GPU, 6.2 .. 6.7 TB/s).
 // Handing the list's end out in short runs instead cost more than it evened out (a run's queries,
 // partial and pages are about 3 us of a warp).
 //

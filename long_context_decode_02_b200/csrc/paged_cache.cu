@@ -5,19 +5,22 @@
 //   s = smallest 2^e >= 2^-64 with amax <= 448 * 2^e;  code = e4m3_rn(x / s),
 // and if the page already holds tokens of the sequence, s is at least the page's scale and the
 // earlier codes are rounded again to s. With powers of two that second rounding is exact unless
-// the code becomes subnormal, so it does not matter (to 2^-10 s) in how many calls a page was
-// filled; a scale amax / 448 would gain nothing, since e4m3's steps are relative.
+// the code becomes subnormal, so it does not matter (to one subnormal step, 2^-9 s) in how many
+// calls a page was filled; a scale amax / 448 would gain nothing, since e4m3's steps are relative.
 //
 // Bound by bytes: 2 N H d (es + 1). A warp takes 16 rows of one page and head, keys or values; the
 // 1, 2 or 4 warps of a (page, head) agree on its maximum. A lane holds the same two pairs (four
 // elements) of each of its rows in registers, so the input is read once, and turns its (cos, sin)
 // on from row to row by theta_i: one look-up (four table levels) a warp, four fp64 operations a
-// row and pair, no shared memory. Angles and products are fp64 because e4m3's rounding and the
+// row and pair. Angles and products are fp64 because e4m3's rounding and the
 // scale's power of two are decisions: an fp32 rotation would flip one in about 2^20 of them
 // against the formula. Short-lived CTAs, five an SM, keep the loads in flight; a CTA that went
 // over several (page, head)s and requested the next rows early took twice as long (112 us against
 // 50 for 23.3K tokens of 8 heads, pages of 64, then; 43 now): 128 registers a thread were not
-// enough for both.
+// enough for both. The number of CTAs an SM costs registers too: at d = 128 the kernels of five
+// (bf16, 96 registers) and four (fp32, 128) spill 268 and 160 bytes, with four and three 36 and
+// none, and were slower for it: 44.2 us against 43.4 in bf16, 55.4 against 51.1 in fp32 (d = 64,
+// where neither spills: 27.0 against 24.6, 37.0 against 31.1).
 #include <type_traits>
 
 #include "paged_common.cuh"

@@ -5,12 +5,13 @@
 
 namespace lowram {
 
-// Four e4m3 codes (byte 0 first) to floats, exactly (every e4m3 value is an fp16 value).
+// Two e4m3 codes (byte 0 first) to fp16, exactly (every e4m3 value is an fp16 value).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
+// Four e4m3 codes (byte 0 first) to floats.
 __device__ __forceinline__ void e4m3x4_to_float(uint32_t w, float* o) {
   const uint32_t a = e4m3x2_to_f16x2((uint16_t)(w & 0xffffu));
   const uint32_t b = e4m3x2_to_f16x2((uint16_t)(w >> 16));
@@ -31,9 +32,9 @@ __device__ __forceinline__ uint32_t float4_to_e4m3x4(const float* x) {
 // The paged kernels are launched as programmatic dependents of whatever precedes them in the
 // stream: a kernel's blocks may be set up while the one before still runs, and touch memory only
 // behind grid_dependency_wait(), which returns when the kernels before have ended and their writes
-// are visible. A kernel lets the next be set up only behind its own wait, so whatever the next one
-// does early sees everything older than its predecessor. (Back to back calls of an append and an attend: about 2 us less than plain
-// launches.)
+// are visible. A kernel lets the next be set up only behind its own wait, in every path, so whatever
+// the next one does early (the merge reads the lengths) sees everything older than its predecessor.
+// (Back to back calls of an append and an attend: about 2 us less than plain launches.)
 __device__ __forceinline__ void grid_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
